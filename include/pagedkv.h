@@ -59,6 +59,9 @@ extern "C" {
 #define PKV_STATUS_WAIT_TIMEOUT 4     /* a bounded wait inside a kernel gave up; outputs are not valid */
 #define PKV_STATUS_BAD_SLOT 8         /* an append slot is >= num_blocks * block_size; that token is skipped */
 #define PKV_STATUS_BAD_PREFIX_GROUP 16 /* a prefix-group member's table differs from the group's shared blocks */
+#define PKV_STATUS_BAD_TREE 32        /* a draft's parent is not an earlier draft, or an accepted path does not rise */
+#define PKV_STATUS_OUT_OF_BLOCKS 64   /* kv_tables_grow: the stack holds too few free blocks; nothing was taken */
+#define PKV_STATUS_OUT_OF_SLOTS 128   /* kv_tables_grow: more new tokens than slot_mapping has entries; nothing was taken */
 
 /* Supported shapes of the decode kernels. */
 #define PKV_MAX_GROUP 8               /* num_q_heads / num_kv_heads <= 8 */
@@ -418,6 +421,145 @@ int paged_attn_decode_noalloc(void *out, const void *q, const void *k_cache, con
 int kv_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
                     const int64_t *slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
                     int block_size, int num_blocks, int32_t *d_status, void *stream);
+
+/*
+ * Speculative decoding: verifying a tree of drafted tokens per sequence in one
+ * step ("Deep Dive into vLLM", section 2.2, names parallel sampling and beam
+ * search, where several continuations share one cached context; here the
+ * continuations are drafts that share their ancestors too). A step is
+ *   kv_tables_grow (blocks and slots for the drafts), paged_tree_mask,
+ *   per layer kv_cache_append of the drafts' rows and paged_attn_tree,
+ *   then, once the caller has chosen each sequence's accepted path,
+ *   per layer kv_cache_keep, and kv_tables_trim.
+ * All of it works on device tensors and can be captured into one graph.
+ *
+ * paged_attn_tree: sequence s brings n_s = query_start[s + 1] - query_start[s]
+ * drafts, the LAST n_s of its context_lens[s] cached tokens. Draft i attends
+ * to every committed position 0 .. context_lens[s] - n_s - 1 and to the drafts
+ * j whose bit is set in its row of tree_mask:
+ *   out[query_start[s] + i] = softmax over those positions of scale q.K^T, times V.
+ * The mask need not be a tree's: any set of drafts, also later ones, and rows
+ * that see nothing at all (no bit set and no committed token) give zeros. A
+ * position a row does not see is no part of its result, whatever K and V hold
+ * there, NaN and infinity included. A chain of drafts is causal attention.
+ *
+ * out, q        device bf16 [num_tokens][num_q_heads][head_dim]
+ * query_start   device int32 [num_seqs + 1]: 0, then non-decreasing, ending at
+ *               or before num_tokens (rows behind it are left as they were);
+ *               every n_s <= context_lens[s] and <= max_query_len
+ * tree_mask     device int32 [num_tokens][mask_words]: bit j % 32 of word j / 32
+ *               = draft j of the same sequence is seen; bits past n_s are
+ *               ignored; mask_words * 32 >= max_query_len
+ * max_query_len host int: the largest n_s, at most PKV_MAX_TREE_TOKENS
+ * workspace     device, pkv_tree_workspace_bytes() bytes, 256-byte aligned; its
+ *               first int32 is the status word, ORed and never cleared by this
+ *               call. Calls that may overlap need one each.
+ * A sequence whose query_start or context length is inconsistent is skipped
+ * (its rows are left as they were) and sets PKV_STATUS_BAD_CONTEXT_LEN; a bad
+ * table entry sets PKV_STATUS_BAD_BLOCK_ID and its positions are not seen.
+ * Supported: as paged_attn_decode, with any number of sequences.
+ *
+ * paged_attn_tree_fp8: the same over e4m3 pools with per-kv-head scales.
+ */
+#define PKV_MAX_TREE_TOKENS 4096
+int pkv_tree_workspace_bytes(int head_dim, size_t *bytes);
+
+int paged_attn_tree(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                    const int32_t *context_lens, const int32_t *query_start, const int32_t *tree_mask, int mask_words,
+                    int num_seqs, int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
+                    int block_size, float scale, int max_blocks_per_seq, int num_blocks, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+int paged_attn_tree_fp8(void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                        const float *v_scale, const int32_t *block_tables, const int32_t *context_lens,
+                        const int32_t *query_start, const int32_t *tree_mask, int mask_words, int num_seqs,
+                        int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
+                        int block_size, float scale, int max_blocks_per_seq, int num_blocks, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * The mask and depths of drafted trees. parents (device int32 [num_tokens]):
+ * draft i's parent is the earlier draft parents[query_start[s] + i] < i of the
+ * same sequence, or -1 where it continues the committed context. Row i of
+ * tree_mask gets the bits of i and all its ancestors (every other bit of its
+ * mask_words words is 0); depths[i] = its number of ancestors, so that the
+ * token's position is context_lens[s] - n_s + depth. Rows behind the last
+ * sequence are left as they were. A parent that is neither -1 nor an earlier
+ * draft counts as -1 and sets PKV_STATUS_BAD_TREE in *d_status; a sequence
+ * whose query_start is inconsistent (or longer than max_query_len <=
+ * mask_words * 32) is skipped and sets PKV_STATUS_BAD_CONTEXT_LEN.
+ */
+int paged_tree_mask(int32_t *tree_mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
+                    int num_seqs, int num_tokens, int max_query_len, int mask_words, int32_t *d_status,
+                    void *stream);
+
+/*
+ * Block tables and slots from request lengths, on the GPU: sequence s, which
+ * holds context_lens[s] tokens, gets room for new_tokens[s] more.
+ *
+ * block_tables  device int32 [num_seqs][max_blocks_per_seq], updated: the
+ *               entries of the new blocks are written, no others
+ * free_blocks   device int32 [num_blocks]: a stack of the pool's free blocks,
+ *               *num_free of them (device int32), the top one last. Blocks are
+ *               taken from the top, sequence after sequence.
+ * new_lens      device int32 [num_seqs]: context_lens + new_tokens
+ * query_start   device int32 [num_seqs + 1]: prefix sums of new_tokens
+ * slot_mapping  device int64 [num_slots]: the slots of the new tokens in order,
+ *               as kv_cache_append takes them; -1 behind the last one
+ * num_free_out  device int32: the blocks left
+ * new_lens may be context_lens, and num_free_out may be num_free; no other
+ * output may overlap an input.
+ * All or nothing: a length that is negative or past the table
+ * (PKV_STATUS_BAD_CONTEXT_LEN), too few blocks (PKV_STATUS_OUT_OF_BLOCKS) or
+ * slots (PKV_STATUS_OUT_OF_SLOTS), or *num_free outside [0, num_blocks]
+ * (PKV_STATUS_BAD_BLOCK_ID) set their bits in *d_status, and the step is then
+ * empty: lengths, tables and stack unchanged, query_start all 0, every slot -1.
+ * A block id on the stack or in a partly filled block's table entry that is
+ * outside the pool gives slot -1 and sets PKV_STATUS_BAD_BLOCK_ID.
+ * Blocks are the sequence's own: a block shared by several tables (see the
+ * host manager, whose reference counts these calls do not know) must be full.
+ */
+int kv_tables_grow(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_tokens,
+                   const int32_t *free_blocks, const int32_t *num_free, int32_t *new_lens, int32_t *query_start,
+                   int64_t *slot_mapping, int32_t *num_free_out, int num_seqs, int num_slots, int max_blocks_per_seq,
+                   int block_size, int num_blocks, int32_t *d_status, void *stream);
+
+/*
+ * Gives back the blocks that fall empty when sequence s keeps its first
+ * keep_lens[s] tokens of context_lens[s] (0: a finished request). They go onto
+ * the stack in the reverse order of kv_tables_grow's taking, so that a grow
+ * undone by a trim leaves stack and count as they were; num_free_out may be
+ * num_free. Table entries are left as they are (entries past a length are
+ * never read). All or nothing: a bad length sets PKV_STATUS_BAD_CONTEXT_LEN, a
+ * stack that would overflow (a block given back twice) PKV_STATUS_BAD_BLOCK_ID,
+ * and nothing changes. An entry outside the pool goes onto the stack as -1 and
+ * sets PKV_STATUS_BAD_BLOCK_ID. Blocks shared with another table must be kept.
+ */
+int kv_tables_trim(const int32_t *block_tables, const int32_t *context_lens, const int32_t *keep_lens,
+                   int32_t *free_blocks, const int32_t *num_free, int32_t *num_free_out, int num_seqs,
+                   int max_blocks_per_seq, int block_size, int num_blocks, int32_t *d_status, void *stream);
+
+/*
+ * Keeps the accepted path of each sequence's drafts: with base =
+ * context_lens[s] - n_s, the K and V rows (all kv heads) of positions base +
+ * accepted[s][k] move to base + k for k < num_accepted[s], bit for bit.
+ *
+ * k_cache, v_cache  pools of elem_bytes-byte elements (2 bf16, 1 e4m3), updated
+ * accepted      device int32 [num_seqs][max_accepted]: the path's drafts in
+ *               rising order, each in [0, n_s)
+ * num_accepted  device int32 [num_seqs]: 0 .. min(n_s, max_accepted)
+ * new_lens      device int32 [num_seqs] or NULL: base + num_accepted[s]; not
+ *               context_lens, which the other layers' calls still read
+ * A sequence with a path that does not rise or leaves its drafts
+ * (PKV_STATUS_BAD_TREE), bad lengths (PKV_STATUS_BAD_CONTEXT_LEN) or a bad
+ * table entry (PKV_STATUS_BAD_BLOCK_ID) keeps its rows, and new_lens[s] =
+ * context_lens[s]. The caller guarantees that no other sequence reads a slot
+ * that is written.
+ */
+int kv_cache_keep(void *k_cache, void *v_cache, const int32_t *block_tables, const int32_t *context_lens,
+                  const int32_t *query_start, const int32_t *accepted, const int32_t *num_accepted, int32_t *new_lens,
+                  int num_seqs, int max_accepted, int num_kv_heads, int head_dim, int elem_bytes, int block_size,
+                  int max_blocks_per_seq, int num_blocks, int32_t *d_status, void *stream);
 
 /*
  * Device check of a batch's tables: ORs PKV_STATUS_BAD_CONTEXT_LEN for any

@@ -37,6 +37,20 @@ from ._binding import (  # noqa: F401
     workspace_bytes,
 )
 from .block_manager import BlockManager, OutOfBlocks, kv_block_copy  # noqa: F401
+from .tree import (  # noqa: F401
+    PKV_MAX_TREE_TOKENS,
+    PKV_STATUS_BAD_TREE,
+    PKV_STATUS_OUT_OF_BLOCKS,
+    PKV_STATUS_OUT_OF_SLOTS,
+    allocate_tree_workspace,
+    kv_cache_keep,
+    kv_tables_grow,
+    kv_tables_trim,
+    paged_attn_tree,
+    paged_attn_tree_fp8,
+    paged_tree_mask,
+    tree_workspace_bytes,
+)
 
 __all__ = [
     "BlockManager",
@@ -45,10 +59,14 @@ __all__ = [
     "OutOfBlocks",
     "PagedKVError",
     "PrefixGroups",
+    "allocate_tree_workspace",
     "allocate_workspace",
     "find_prefix_groups",
     "kv_block_copy",
     "kv_cache_append",
+    "kv_cache_keep",
+    "kv_tables_grow",
+    "kv_tables_trim",
     "library",
     "library_path",
     "paged_attn_decode",
@@ -57,8 +75,12 @@ __all__ = [
     "paged_attn_decode_fp8",
     "paged_attn_decode_noalloc",
     "paged_attn_prefill",
+    "paged_attn_tree",
+    "paged_attn_tree_fp8",
+    "paged_tree_mask",
     "kv_cache_append_fp8",
     "read_status",
+    "tree_workspace_bytes",
     "validate",
     "workspace_bytes",
 ]

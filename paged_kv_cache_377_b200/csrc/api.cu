@@ -703,6 +703,211 @@ int kv_block_copy(void *k_cache, void *v_cache, const int32_t *src, const int32_
     return ok();
 }
 
+int pkv_tree_workspace_bytes(int head_dim, size_t *bytes) {
+    if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    if (head_dim != 64 && head_dim != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "head_dim %d not supported (64 or 128)", head_dim);
+    *bytes = pkv::kWorkspaceHeaderBytes;
+    return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// paged_attn_tree over bf16 pools (k_scale == nullptr) or e4m3 pools.
+int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+              const float *v_scale, const int32_t *block_tables, const int32_t *context_lens,
+              const int32_t *query_start, const int32_t *tree_mask, int mask_words, int num_seqs, int num_tokens,
+              int max_query_len, int num_q_heads, int num_kv_heads, int head_dim, int block_size, float scale,
+              int max_blocks_per_seq, int num_blocks, void *workspace, size_t workspace_bytes, void *stream) {
+    if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "num_seqs, num_tokens and max_query_len must be >= 0");
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return ok();  // empty arrays may be NULL
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !tree_mask ||
+        !workspace || (fp8 && (!k_scale || !v_scale)))
+        return fail(PKV_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 ||
+        num_blocks <= 0 || mask_words <= 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "head counts, head_dim, block_size, max_blocks_per_seq, num_blocks and "
+                                              "mask_words must be positive");
+    if (num_q_heads % num_kv_heads != 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "num_q_heads %d is not a multiple of num_kv_heads %d", num_q_heads,
+                    num_kv_heads);
+    if (!std::isfinite(scale)) return fail(PKV_ERR_INVALID_ARGUMENT, "scale is not finite");
+    const int group = num_q_heads / num_kv_heads;
+    if (head_dim != 64 && head_dim != 128)
+        return fail(PKV_ERR_UNSUPPORTED, "head_dim %d not supported (64 or 128)", head_dim);
+    if (block_size != 16 && block_size != 32)
+        return fail(PKV_ERR_UNSUPPORTED, "block_size %d not supported (16 or 32)", block_size);
+    if (group > PKV_MAX_GROUP)
+        return fail(PKV_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads = %d exceeds %d", group, PKV_MAX_GROUP);
+    if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffff ||
+        static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffff)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "pool or table too large: blocks * block_size must be < 2^31");
+    if (max_query_len > PKV_MAX_TREE_TOKENS)
+        return fail(PKV_ERR_UNSUPPORTED, "max_query_len %d exceeds %d", max_query_len, PKV_MAX_TREE_TOKENS);
+    if (max_query_len > static_cast<int64_t>(mask_words) * 32)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "mask_words %d hold fewer bits than max_query_len %d", mask_words,
+                    max_query_len);
+    if (static_cast<int64_t>(num_tokens) * num_q_heads * head_dim > (int64_t(1) << 40))
+        return fail(PKV_ERR_INVALID_ARGUMENT, "num_tokens too large");
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(workspace, 256))
+        return fail(PKV_ERR_INVALID_ARGUMENT,
+                    "out, q, k_cache and v_cache must be 16-byte aligned, workspace 256-byte aligned");
+    size_t need = 0;
+    int rc = pkv_tree_workspace_bytes(head_dim, &need);
+    if (rc != PKV_OK) return rc;
+    if (workspace_bytes < need)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "workspace_bytes %zu < %zu", workspace_bytes, need);
+    pkv::TreeArgs a{};
+    a.out = out;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start = query_start;
+    a.tree_mask = tree_mask;
+    a.status = static_cast<int32_t *>(workspace);
+    a.num_seqs = num_seqs;
+    a.num_tokens = num_tokens;
+    a.max_query_len = max_query_len;
+    a.mask_words = mask_words;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.group = group;
+    a.block_size = block_size;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    const cudaError_t e = pkv::tree_launch(fp8, head_dim, a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int paged_attn_tree(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                    const int32_t *context_lens, const int32_t *query_start, const int32_t *tree_mask, int mask_words,
+                    int num_seqs, int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
+                    int block_size, float scale, int max_blocks_per_seq, int num_blocks, void *workspace,
+                    size_t workspace_bytes, void *stream) {
+    return tree_impl(false, out, q, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, query_start,
+                     tree_mask, mask_words, num_seqs, num_tokens, max_query_len, num_q_heads, num_kv_heads, head_dim,
+                     block_size, scale, max_blocks_per_seq, num_blocks, workspace, workspace_bytes, stream);
+}
+
+int paged_attn_tree_fp8(void *out, const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                        const float *v_scale, const int32_t *block_tables, const int32_t *context_lens,
+                        const int32_t *query_start, const int32_t *tree_mask, int mask_words, int num_seqs,
+                        int num_tokens, int max_query_len, int num_q_heads, int num_kv_heads, int head_dim,
+                        int block_size, float scale, int max_blocks_per_seq, int num_blocks, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    return tree_impl(true, out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, query_start,
+                     tree_mask, mask_words, num_seqs, num_tokens, max_query_len, num_q_heads, num_kv_heads, head_dim,
+                     block_size, scale, max_blocks_per_seq, num_blocks, workspace, workspace_bytes, stream);
+}
+
+int paged_tree_mask(int32_t *tree_mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
+                    int num_seqs, int num_tokens, int max_query_len, int mask_words, int32_t *d_status,
+                    void *stream) {
+    if (num_seqs < 0 || num_tokens < 0 || max_query_len < 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "num_seqs, num_tokens and max_query_len must be >= 0");
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return ok();  // empty arrays may be NULL
+    if (!tree_mask || !depths || !parents || !query_start || !d_status)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (mask_words <= 0) return fail(PKV_ERR_INVALID_ARGUMENT, "mask_words must be positive");
+    if (max_query_len > PKV_MAX_TREE_TOKENS)
+        return fail(PKV_ERR_UNSUPPORTED, "max_query_len %d exceeds %d", max_query_len, PKV_MAX_TREE_TOKENS);
+    if (max_query_len > static_cast<int64_t>(mask_words) * 32)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "mask_words %d hold fewer bits than max_query_len %d", mask_words,
+                    max_query_len);
+    const cudaError_t e = pkv::tree_mask_launch(tree_mask, depths, parents, query_start, num_seqs, num_tokens,
+                                                max_query_len, mask_words, d_status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "tree mask launch");
+    return ok();
+}
+
+int kv_tables_grow(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_tokens,
+                   const int32_t *free_blocks, const int32_t *num_free, int32_t *new_lens, int32_t *query_start,
+                   int64_t *slot_mapping, int32_t *num_free_out, int num_seqs, int num_slots, int max_blocks_per_seq,
+                   int block_size, int num_blocks, int32_t *d_status, void *stream) {
+    if (num_seqs < 0 || num_slots < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_seqs and num_slots must be >= 0");
+    if (!free_blocks || !num_free || !query_start || !num_free_out || !d_status || (num_slots > 0 && !slot_mapping) ||
+        (num_seqs > 0 && (!block_tables || !context_lens || !new_tokens || !new_lens)))
+        return fail(PKV_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (max_blocks_per_seq <= 0 || block_size <= 0 || num_blocks <= 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "max_blocks_per_seq, block_size and num_blocks must be positive");
+    if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffff ||
+        static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffff)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "pool or table too large: blocks * block_size must be < 2^31");
+    if (num_slots > (1 << 30)) return fail(PKV_ERR_INVALID_ARGUMENT, "num_slots too large (at most 2^30)");
+    const cudaError_t e = pkv::tables_grow_launch(
+        block_tables, context_lens, new_tokens, free_blocks, num_free, new_lens, query_start, slot_mapping,
+        num_free_out, num_seqs, num_slots, max_blocks_per_seq, block_size, num_blocks, d_status,
+        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "table growth launch");
+    return ok();
+}
+
+int kv_tables_trim(const int32_t *block_tables, const int32_t *context_lens, const int32_t *keep_lens,
+                   int32_t *free_blocks, const int32_t *num_free, int32_t *num_free_out, int num_seqs,
+                   int max_blocks_per_seq, int block_size, int num_blocks, int32_t *d_status, void *stream) {
+    if (num_seqs < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_seqs < 0");
+    if (!free_blocks || !num_free || !num_free_out || !d_status ||
+        (num_seqs > 0 && (!block_tables || !context_lens || !keep_lens)))
+        return fail(PKV_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (max_blocks_per_seq <= 0 || block_size <= 0 || num_blocks <= 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "max_blocks_per_seq, block_size and num_blocks must be positive");
+    if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffff ||
+        static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffff)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "pool or table too large: blocks * block_size must be < 2^31");
+    const cudaError_t e =
+        pkv::tables_trim_launch(block_tables, context_lens, keep_lens, free_blocks, num_free, num_free_out, num_seqs,
+                                max_blocks_per_seq, block_size, num_blocks, d_status, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "table trim launch");
+    return ok();
+}
+
+int kv_cache_keep(void *k_cache, void *v_cache, const int32_t *block_tables, const int32_t *context_lens,
+                  const int32_t *query_start, const int32_t *accepted, const int32_t *num_accepted, int32_t *new_lens,
+                  int num_seqs, int max_accepted, int num_kv_heads, int head_dim, int elem_bytes, int block_size,
+                  int max_blocks_per_seq, int num_blocks, int32_t *d_status, void *stream) {
+    if (num_seqs < 0 || max_accepted < 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "num_seqs and max_accepted must be >= 0");
+    if (num_seqs == 0) return ok();  // empty arrays may be NULL
+    if (!k_cache || !v_cache || !block_tables || !context_lens || !query_start || !num_accepted || !d_status ||
+        (max_accepted > 0 && !accepted))
+        return fail(PKV_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (num_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0)
+        return fail(PKV_ERR_INVALID_ARGUMENT,
+                    "num_kv_heads, head_dim, block_size, num_blocks and max_blocks_per_seq must be positive");
+    if (elem_bytes != 1 && elem_bytes != 2) return fail(PKV_ERR_INVALID_ARGUMENT, "elem_bytes must be 1 or 2");
+    const int64_t row_bytes = static_cast<int64_t>(num_kv_heads) * head_dim * elem_bytes;
+    if (static_cast<int64_t>(head_dim) * elem_bytes % 16 != 0)
+        return fail(PKV_ERR_UNSUPPORTED, "a row of head_dim %d is not a multiple of 16 bytes", head_dim);
+    if (row_bytes > (1 << 26)) return fail(PKV_ERR_UNSUPPORTED, "a token's heads take more than 2^26 bytes");
+    if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffff ||
+        static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffff)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "pool or table too large: blocks * block_size must be < 2^31");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return fail(PKV_ERR_INVALID_ARGUMENT, "k_cache and v_cache must be 16-byte aligned");
+    if (new_lens == context_lens)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "new_lens must not be context_lens: the next layer still reads them");
+    const cudaError_t e = pkv::cache_keep_launch(
+        k_cache, v_cache, block_tables, context_lens, query_start, accepted, num_accepted, new_lens, num_seqs,
+        max_accepted, static_cast<int>(row_bytes), block_size, max_blocks_per_seq, num_blocks, d_status,
+        static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "path move launch");
+    return ok();
+}
+
 int pkv_validate(const int32_t *block_tables, const int32_t *context_lens, int num_seqs, int max_blocks_per_seq,
                  int block_size, int num_blocks, int32_t *d_status, void *stream) {
     if (num_seqs < 0) return fail(PKV_ERR_INVALID_ARGUMENT, "num_seqs < 0");

@@ -61,6 +61,44 @@ cudaError_t prefill_tc_launch(int head_dim, int block_size, const CUtensorMap &t
                               cudaStream_t stream);
 int prefill_tc_rows_per_cta();
 
+// Attention of drafted trees (tree.cu).
+struct TreeArgs {
+    void *out;                    // bf16 [T][Hq][D]
+    const void *q;                // bf16 [T][Hq][D]
+    const void *k_cache;          // [NB][BS][Hkv][D], bf16 or e4m3 codes
+    const void *v_cache;
+    const float *k_scale;         // e4m3 pools: fp32 [Hkv]
+    const float *v_scale;
+    const int32_t *block_tables;  // [S][MB]
+    const int32_t *context_lens;  // [S], the drafts included
+    const int32_t *query_start;   // [S + 1]
+    const int32_t *tree_mask;     // [T][mask_words]
+    int32_t *status;
+    int num_seqs, num_tokens, max_query_len, mask_words, num_q_heads, num_kv_heads, group, block_size,
+        max_blocks_per_seq, num_blocks;
+    float scale_log2;
+};
+
+cudaError_t tree_launch(bool fp8, int head_dim, const TreeArgs &args, cudaStream_t stream);
+
+// A step's bookkeeping on the GPU (tables.cu).
+cudaError_t tables_grow_launch(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_tokens,
+                               const int32_t *free_blocks, const int32_t *num_free, int32_t *new_lens,
+                               int32_t *query_start, int64_t *slot_mapping, int32_t *num_free_out, int num_seqs,
+                               int num_slots, int max_blocks_per_seq, int block_size, int num_blocks, int32_t *status,
+                               cudaStream_t stream);
+cudaError_t tables_trim_launch(const int32_t *block_tables, const int32_t *context_lens, const int32_t *keep_lens,
+                               int32_t *free_blocks, const int32_t *num_free, int32_t *num_free_out, int num_seqs,
+                               int max_blocks_per_seq, int block_size, int num_blocks, int32_t *status,
+                               cudaStream_t stream);
+cudaError_t tree_mask_launch(int32_t *tree_mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
+                             int num_seqs, int num_tokens, int max_query_len, int mask_words, int32_t *status,
+                             cudaStream_t stream);
+cudaError_t cache_keep_launch(void *k_cache, void *v_cache, const int32_t *block_tables, const int32_t *context_lens,
+                              const int32_t *query_start, const int32_t *accepted, const int32_t *num_accepted,
+                              int32_t *new_lens, int num_seqs, int max_accepted, int row_bytes, int block_size,
+                              int max_blocks_per_seq, int num_blocks, int32_t *status, cudaStream_t stream);
+
 cudaError_t append_fp8_launch(const void *k, const void *v, void *k_cache, void *v_cache, const int64_t *slot_mapping,
                               const float *k_scale, const float *v_scale, int num_tokens, int num_kv_heads,
                               int head_dim, int block_size, int num_blocks, int32_t *status, cudaStream_t stream);
