@@ -703,11 +703,35 @@ int kv_block_copy(void *k_cache, void *v_cache, const int32_t *src, const int32_
     return ok();
 }
 
+}  // extern "C"
+
+namespace {
+
+// Tree workspace: [0, 256) header (status word at 0) | the CTAs' cut segments | rows' maxima and sums of the
+// partials | their fp32 rows. Two partials of 128 rows for each of kTreeMaxCtas CTAs (or of 256 for half as many).
+struct TreeLayout {
+    size_t cuts, ml_part, o_part, total;
+};
+
+TreeLayout tree_layout(int head_dim) {
+    const size_t rows = 2 * 128 * static_cast<size_t>(pkv::kTreeMaxCtas);
+    TreeLayout w;
+    w.cuts = pkv::kWorkspaceHeaderBytes;
+    w.ml_part = w.cuts + pkv::kTreeMaxCtas * sizeof(int4);
+    w.o_part = w.ml_part + rows * sizeof(float2);
+    w.total = w.o_part + rows * head_dim * sizeof(float);
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
 int pkv_tree_workspace_bytes(int head_dim, size_t *bytes) {
     if (!bytes) return fail(PKV_ERR_INVALID_ARGUMENT, "bytes is NULL");
     if (head_dim != 64 && head_dim != 128)
         return fail(PKV_ERR_UNSUPPORTED, "head_dim %d not supported (64 or 128)", head_dim);
-    *bytes = pkv::kWorkspaceHeaderBytes;
+    *bytes = tree_layout(head_dim).total;
     return ok();
 }
 
@@ -784,8 +808,46 @@ int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const voi
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.num_blocks = num_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
-    const cudaError_t e = pkv::tree_launch(fp8, head_dim, a, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    if (std::fabs(a.scale_log2) < 1e-30f) a.scale_log2 = 1e-30f;  // hidden logits are -inf: never times zero
+    if (fp8) {
+        const cudaError_t e = pkv::tree_simple_launch(true, head_dim, a, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+        return ok();
+    }
+    CUtensorMap tm_q, tm_k, tm_v;
+    if ((rc = make_pool_map(&tm_k, k_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    if ((rc = make_pool_map(&tm_v, v_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    if ((rc = make_query_map(&tm_q, q, num_tokens, num_kv_heads, group, head_dim)) != PKV_OK) return rc;
+    const TreeLayout lay = tree_layout(head_dim);
+    char *ws = static_cast<char *>(workspace);
+    a.cuts = reinterpret_cast<int4 *>(ws + lay.cuts);
+    a.ml_part = reinterpret_cast<float2 *>(ws + lay.ml_part);
+    a.o_part = reinterpret_cast<float *>(ws + lay.o_part);
+    const int sms = sm_count();
+    if (sms <= 0) return fail(PKV_ERR_CUDA, "no current device");
+    a.tile_drafts = 128 / group;
+    const int tiles = max_query_len > a.tile_drafts ? 2 : 1;
+    a.group_drafts = tiles * a.tile_drafts;
+    a.piece_cost = 2;
+    a.min_weight = 4;
+    const int64_t most_it = (static_cast<int64_t>(max_blocks_per_seq) * block_size + 63) / 64;
+    a.whole = most_it <= 8;
+    const int groups = (max_query_len + a.group_drafts - 1) / a.group_drafts;
+    for (int s0 = 0; s0 < num_seqs; s0 += pkv::kTreeMaxSeqs) {
+        a.num_seqs = num_seqs - s0 < pkv::kTreeMaxSeqs ? num_seqs - s0 : pkv::kTreeMaxSeqs;
+        a.block_tables = block_tables + static_cast<int64_t>(s0) * max_blocks_per_seq;
+        a.context_lens = context_lens + s0;
+        a.query_start = query_start + s0;
+        // one wave of CTAs, or fewer where the tables bound the work
+        const int64_t segments = static_cast<int64_t>(a.num_seqs) * num_kv_heads * groups;
+        const int64_t bound = a.whole ? segments : segments * (most_it + a.piece_cost) / a.min_weight + 1;
+        int64_t ctas = static_cast<int64_t>(sms) * (tiles == 1 ? 2 : 1);
+        if (ctas > pkv::kTreeMaxCtas / tiles) ctas = pkv::kTreeMaxCtas / tiles;
+        if (ctas > bound) ctas = bound;
+        const cudaError_t e = pkv::tree_launch(head_dim, tm_q, tm_k, tm_v, a, static_cast<int>(ctas),
+                                               static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    }
     return ok();
 }
 

@@ -76,10 +76,23 @@ struct TreeArgs {
     int32_t *status;
     int num_seqs, num_tokens, max_query_len, mask_words, num_q_heads, num_kv_heads, group, block_size,
         max_blocks_per_seq, num_blocks;
-    float scale_log2;
+    float scale_log2;             // not zero
+    int tile_drafts;              // drafts of a 128-row tile: 128 / group
+    int group_drafts;             // drafts that share a pass over K and V: one tile's or two tiles'
+    int piece_cost;               // a segment's fixed weight, in iterations
+    int min_weight;               // iterations that make another CTA worth it
+    int whole;                    // 1: no segment is cut
+    float *o_part;                // fp32 [2 * CTAs][rows][D]: each CTA's partials of a continued and of a begun segment
+    float2 *ml_part;              // their rows' maximum (log2 domain) and sum
+    int4 *cuts;                   // [CTAs]: the cut segment that a CTA begins (see tree_merge_kernel)
 };
 
-cudaError_t tree_launch(bool fp8, int head_dim, const TreeArgs &args, cudaStream_t stream);
+constexpr int kTreeMaxSeqs = 1024;  // sequences of one launch (weights kept in shared memory)
+constexpr int kTreeMaxCtas = 320;   // one-tile CTAs; half as many of two tiles
+
+cudaError_t tree_launch(int head_dim, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                        const TreeArgs &args, int ctas, cudaStream_t stream);
+cudaError_t tree_simple_launch(bool fp8, int head_dim, const TreeArgs &args, cudaStream_t stream);
 
 // A step's bookkeeping on the GPU (tables.cu).
 cudaError_t tables_grow_launch(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_tokens,
