@@ -15,10 +15,10 @@
 // maximum and the sum of each row), which tree_merge_kernel joins.
 //
 // Roles, each walking the CTA's share on its own: one warp brings Q and K by
-// TMA, one V, one issues the MMAs (S = Q K^T into tensor memory, O += P V with P
-// read from there), and four warps per row tile hold a row per thread: they
+// TMA, one V, one per row tile issues its MMAs (S = Q K^T into tensor memory, O +=
+// P V with P read from there), and four warps per row tile hold a row per thread: they
 // load its 64 logits, hide what the row does not see, keep the running maximum
-// and sum in fp32, and write P in bf16 over S. The mask only matters in the
+// and sum in fp32, and write P in bf16 beside S. The mask only matters in the
 // iterations that reach past the committed tokens: a row's bits for 64 positions
 // are two words there.
 #include <cuda_bf16.h>
@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kRows = 128;       // rows of a tile (= tensor-memory lanes)
 constexpr int kTokens = 64;      // positions of one iteration
-constexpr int kBadRing = 8;      // iterations whose bad-block bits are kept
+constexpr int kBadRing = 8;      // iterations whose bad-block bits are kept (a loader is at most 5 ahead)
+constexpr int kPoisonRing = 16;  // pieces whose flag is kept (one tile's warps are at most 6 ahead of the other's)
 
 // A CTA's share of the step, piece by piece (a piece: consecutive iterations of
 // one segment). Every role walks it alike.
@@ -116,17 +117,19 @@ struct TreeShape {
 };
 
 constexpr int tree_stages(int tiles) { return tiles == 1 ? 2 : 4; }
-constexpr int tree_threads(int tiles) { return tiles * 128 + 96; }
+constexpr int tree_threads(int tiles) { return tiles * 160 + 64; }
 
 struct TreeBars {
-    uint64_t q_full, q_empty, done;
+    uint64_t q_full, q_empty, done[2];
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2][2], p_ready[2][2], pv_free[2][2], o_full[2];
+    // per tile: S is in tensor memory; the softmax threads have loaded it; P (buffer b) is written; O += P V
+    // of buffer b is done; the piece's O is done
+    uint64_t s_full[2], s_free[2], p_ready[2][2], pv_free[2][2], o_full[2];
     int64_t scan[16];
     uint32_t bad[kBadRing];
     uint32_t tmem;
     int abort;
-    int poison[4];
+    int poison[kPoisonRing];
 };
 
 template <int D, int BS, int TILES>
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                       const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
     using Sh = TreeShape<D>;
     constexpr int HALVES = Sh::HALVES, BPI = kTokens / BS, STAGES = tree_stages(TILES);
-    constexpr int kThreads = tree_threads(TILES), kLoadK = 4 * TILES, kMma = kLoadK + 1, kLoadV = kLoadK + 2;
+    constexpr int kThreads = tree_threads(TILES), kLoadK = 4 * TILES, kLoadV = kLoadK + 1, kMma = kLoadK + 2;
     constexpr uint32_t kTmemCols = 256 * TILES;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -207,30 +210,31 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
         walk.s = lo;
     }
 
-    if (warp == kMma) {
+    if (warp == kMma) {  // all of the CTA's columns
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)),
                      "r"(kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
         tc_fence_before();
     } else if (warp == kLoadK && lane == 0) {
         mbar_init(&B.q_full, 1);
-        mbar_init(&B.q_empty, 1);
-        mbar_init(&B.done, 1);
+        mbar_init(&B.q_empty, TILES);
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(&B.k_full[i], 1);
-            mbar_init(&B.k_empty[i], 1);
+            mbar_init(&B.k_empty[i], TILES);
             mbar_init(&B.v_full[i], 1);
-            mbar_init(&B.v_empty[i], 1);
+            mbar_init(&B.v_empty[i], TILES);
         }
         for (int t = 0; t < TILES; ++t) {
+            mbar_init(&B.done[t], 1);
+            mbar_init(&B.s_full[t], 1);
+            mbar_init(&B.s_free[t], 128);
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&B.s_full[t][i], 1);
                 mbar_init(&B.p_ready[t][i], 128);
                 mbar_init(&B.pv_free[t][i], 1);
             }
             mbar_init(&B.o_full[t], 1);
         }
-        for (int i = 0; i < 4; ++i) B.poison[i] = 0;
+        for (int i = 0; i < kPoisonRing; ++i) B.poison[i] = 0;
         B.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -305,69 +309,68 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                 mbar_wait_drain(&full[u % STAGES], (u / STAGES) & 1u, a.status);
         }
         __syncwarp();
-    } else if (warp == kMma) {
-        // ---------------- MMA warp: one elected lane issues. S runs one iteration ahead of P V.
+    } else if (warp >= kMma) {
+        // ---------------- MMA warp of tile t: one elected lane issues. S(it + 1) is issued as soon as the softmax
+        // warps hold S(it) in registers, and runs while they work on it; O += P(it) V(it) follows P(it).
+        const int t = TILES == 1 ? 0 : warp - kMma;
         const bool leader = elect_one();
-        const uint64_t dq = smem_desc(smem_u32(sq), 16, 1024), dk = smem_desc(smem_u32(sk), 16, 1024),
+        const uint64_t dq = smem_desc(smem_u32(sq + t * Sh::kTileQ), 16, 1024), dk = smem_desc(smem_u32(sk), 16, 1024),
                        dv = smem_desc(smem_u32(sv), Sh::kHalfKV, 1024);
+        const uint32_t t_s = tbase + 256 * t, t_p = t_s + 64, t_o = t_s + 128;
         Walk ws = walk, wv = walk;
-        uint32_t gs = 0, gv = 0, pieces = 0;
-        uint32_t us[TILES] = {}, uv[TILES] = {};  // uses of each tile's S / P buffers
+        uint32_t gs = 0, gv = 0, pieces = 0, us = 0, uv = 0;  // iterations, pieces; iterations with a live tile
         bool ok = true;
         auto step_s = [&]() {
-            const int st = gs % STAGES, tiles = TILES == 1 ? 1 : ws.tiles(a);
+            const int st = gs % STAGES;
+            const bool last = ws.it + 1 == ws.it1, live = t < ws.tiles(a);
             if (ws.it == ws.it0) {
                 if (!(ok = warp_wait(&B.q_full, pieces & 1u, abort_flag, a.status))) return;
                 ++pieces;
             }
             if (!(ok = warp_wait(&B.k_full[st], (gs / STAGES) & 1u, abort_flag, a.status))) return;
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-                if (t >= tiles) break;
-                const uint32_t b = us[t] & 1u;
-                if (us[t] >= 2 && !(ok = warp_wait(&B.pv_free[t][b], ((us[t] >> 1) - 1) & 1u, abort_flag, a.status)))
-                    return;
+            if (live) {
+                if (us > 0 && !(ok = warp_wait(&B.s_free[t], (us - 1) & 1u, abort_flag, a.status))) return;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
                     for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma(tbase + 256 * t + 64 * b, dq + ((t * Sh::kTileQ + hf * Sh::kQHalf + kk * 32) >> 4),
+                            umma(t_s, dq + ((hf * Sh::kQHalf + kk * 32) >> 4),
                                  dk + ((st * Sh::kTileKV + hf * Sh::kHalfKV + kk * 32) >> 4),
                                  instr_desc(128, kTokens, false), (hf | kk) != 0);
-                    umma_commit(&B.s_full[t][b]);
+                    umma_commit(&B.s_full[t]);
+                    umma_commit(&B.k_empty[st]);
+                    if (last) umma_commit(&B.q_empty);
                 }
-                ++us[t];
-            }
-            if (leader) {
-                umma_commit(&B.k_empty[st]);
-                if (ws.it + 1 == ws.it1) umma_commit(&B.q_empty);
+                ++us;
+            } else if (lane == 0) {
+                mbar_arrive(&B.k_empty[st]);
+                if (last) mbar_arrive(&B.q_empty);
             }
             __syncwarp();
             ++gs;
         };
         auto step_v = [&]() {
-            const int st = gv % STAGES, tiles = TILES == 1 ? 1 : wv.tiles(a);
+            const int st = gv % STAGES;
+            const uint32_t b = uv & 1u;
             if (!(ok = warp_wait(&B.v_full[st], (gv / STAGES) & 1u, abort_flag, a.status))) return;
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-                if (t >= tiles) break;
-                const uint32_t b = uv[t] & 1u;
-                if (!(ok = warp_wait(&B.p_ready[t][b], (uv[t] >> 1) & 1u, abort_flag, a.status))) return;
+            if (t < wv.tiles(a)) {
+                if (!(ok = warp_wait(&B.p_ready[t][b], (uv >> 1) & 1u, abort_flag, a.status))) return;
                 tc_fence_after();
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_ts(tbase + 256 * t + 128, tbase + 256 * t + 64 * b + kk * 8,
-                                dv + ((st * Sh::kTileKV + kk * 16 * 128) >> 4), instr_desc(128, D, true),
-                                wv.it != wv.it0 || kk != 0);
+                        umma_ts(t_o, t_p + 32 * b + kk * 8, dv + ((st * Sh::kTileKV + kk * 16 * 128) >> 4),
+                                instr_desc(128, D, true), wv.it != wv.it0 || kk != 0);
                     umma_commit(&B.pv_free[t][b]);
+                    umma_commit(&B.v_empty[st]);
                     if (wv.it + 1 == wv.it1) umma_commit(&B.o_full[t]);
                 }
-                ++uv[t];
+                ++uv;
+            } else if (lane == 0) {
+                mbar_arrive(&B.v_empty[st]);
             }
-            if (leader) umma_commit(&B.v_empty[st]);
             __syncwarp();
             ++gv;
         };
@@ -387,17 +390,18 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
             more_v = wv.next(a, wp);
         }
         // every MMA issued is done before the tensor memory is freed (one phase: nothing aliases)
-        if (leader) umma_commit(&B.done);
+        if (leader) umma_commit(&B.done[t]);
         __syncwarp();
-        mbar_wait_drain(&B.done, 0, a.status);
+        mbar_wait_drain(&B.done[t], 0, a.status);
         __syncwarp();
     } else {
         // ---------------- softmax warps: thread r of tile t owns a row (tensor-memory lane r)
         const int t = TILES == 1 ? 0 : warp >> 2, r = tid & 127, wlane = (warp & 3) * 32;
-        const uint32_t t_s0 = tbase + 256 * t + (static_cast<uint32_t>(wlane) << 16), t_o = t_s0 + 128;
+        const uint32_t t_s = tbase + 256 * t + (static_cast<uint32_t>(wlane) << 16), t_p = t_s + 64, t_o = t_s + 128;
         const int G = a.group, row_draft = t * a.tile_drafts + r / G;  // draft of this row within the row group
         const float c2 = fabsf(a.scale_log2);
         const bool negative = a.scale_log2 < 0.f, spare = r >= a.tile_drafts * G;
+        volatile int *poison = B.poison;
         uint32_t u = 0, g = 0, mine = 0, pieces = 0;
         bool ok = true;
         while (ok && walk.next_piece(a, wp)) {
@@ -413,15 +417,19 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
             const int32_t *bits = a.tree_mask + static_cast<int64_t>(walk.q0 + min(draft, walk.n - 1)) * a.mask_words;
             float m_ref = -INFINITY, l_run = 0.f;
             for (int it = walk.it0; it < walk.it1; ++it, ++u, ++g) {
-                const uint32_t b = u & 1u, t_s = t_s0 + 64 * b;
+                const uint32_t b = u & 1u;
                 const int t0 = it * kTokens;
-                if (!(ok = warp_wait(&B.s_full[t][b], (u >> 1) & 1u, abort_flag, a.status))) break;
+                if (!(ok = warp_wait(&B.s_full[t], u & 1u, abort_flag, a.status))) break;
                 const uint32_t bad = B.bad[g % kBadRing];
                 const bool tail = t0 + kTokens > first;
-                if (warp_live) {
+                if (!warp_live) {
+                    mbar_arrive(&B.s_free[t]);
+                } else {
                     tc_fence_after();
                     float x[64];
                     tmem_ld64(t_s, x);
+                    tc_fence_before();
+                    mbar_arrive(&B.s_free[t]);
                     if (negative) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i) x[i] = -x[i];
@@ -459,6 +467,8 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                     const float shift = m_new == -INFINITY ? 0.f : -m_new;  // a row that has seen nothing: P = 0
                     const float2 cc = make_float2(c2, c2), nm = make_float2(shift, shift);
                     float2 ps2a = make_float2(0.f, 0.f), ps2b = make_float2(0.f, 0.f);
+                    if (u >= 2 && !(ok = warp_wait(&B.pv_free[t][b], ((u >> 1) - 1) & 1u, abort_flag, a.status))) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         uint32_t w[16];
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                             const __nv_bfloat162 v2 = __floats2bfloat162_rn(pr.x, pr.y);
                             w[e] = *reinterpret_cast<const uint32_t *>(&v2);
                         }
-                        tmem_st16(t_s + 16 * half, w);
+                        tmem_st16(t_p + 32 * b + 16 * half, w);
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     l_run = l_run * alpha + ((ps2a.x + ps2b.x) + (ps2a.y + ps2b.y));
@@ -495,12 +505,12 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                 }
                 // V rows that hold no token (past the context, or of a bad block) may be anything: zero, so that
                 // P = 0 there multiplies zeros. A draft's V that is not finite is hidden from the rows that do not
-                // see it in the same way, and added back to the others at the end.
-                if (t == 0 && (tail || bad)) {
+                // see it in the same way, and added back to the others at the end. Each tile's warps do so before
+                // their own P V; both write the same bytes, the flag always before the first of them.
+                if (tail || bad) {
                     const int st = g % STAGES;
                     if (!(ok = warp_wait(&B.v_full[st], (g / STAGES) & 1u, abort_flag, a.status))) break;
                     uint8_t *vt = sv + st * Sh::kTileKV;
-                    bool odd = false;
                     for (int e = r; e < HALVES * kTokens * 8; e += 128) {
                         const int hf = e / (kTokens * 8), tok = (e / 8) % kTokens, ch = e % 8;
                         uint4 *at = reinterpret_cast<uint4 *>(vt + hf * Sh::kHalfKV + tok * 128 + ((ch ^ (tok & 7)) << 4));
@@ -522,12 +532,13 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                                 }
                             }
                             if (any) {
+                                poison[piece % kPoisonRing] = 1;
+                                __threadfence_block();
                                 *at = v;
-                                odd = true;
                             }
                         }
                     }
-                    if (odd) B.poison[piece & 3u] = 1;
+                    __threadfence_block();
                     fence_proxy_async_shared();
                 }
                 tc_fence_before();
@@ -538,8 +549,8 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
             ++mine;
             tc_fence_after();
             if (*abort_flag) break;
-            const bool poison = *reinterpret_cast<volatile int *>(&B.poison[piece & 3u]) != 0;
-            if (t == 0 && r == 0) B.poison[(piece + 2) & 3u] = 0;
+            const bool poisoned = poison[piece % kPoisonRing] != 0;
+            if (t == 0 && r == 0) poison[(piece + kPoisonRing / 2) % kPoisonRing] = 0;
             const bool cut = walk.it0 > 0 || walk.it1 < walk.nit;
             const int64_t row = static_cast<int64_t>(c) * 2 + (walk.it0 > 0 ? 0 : 1);  // the CTA's partial
             float *part = nullptr;
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                 for (int cb = 0; cb < D / 32; ++cb) {
                     float o[32];
                     tmem_ld32(t_o + cb * 32, o);
-                    if (poison && live) {
+                    if (poisoned && live) {
                         for (int j = max(walk.it0 * kTokens - first, 0); j < min(walk.it1 * kTokens - first, walk.n); ++j) {
                             if (!((bits[j >> 5] >> (j & 31)) & 1)) continue;
                             const int pos = first + j;
