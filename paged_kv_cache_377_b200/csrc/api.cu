@@ -707,17 +707,18 @@ int kv_block_copy(void *k_cache, void *v_cache, const int32_t *src, const int32_
 
 namespace {
 
-// Tree workspace: [0, 256) header (status word at 0) | the CTAs' cut segments | rows' maxima and sums of the
-// partials | their fp32 rows. Two partials of 128 rows for each of kTreeMaxCtas CTAs (or of 256 for half as many).
+// Tree workspace: [0, 256) header (status word at 0) | the CTAs' cut segments | counters of two-piece segments | rows' maxima and sums of the
+// partials | their fp32 rows: two partials of 128 rows for each of kTreeMaxCtas CTAs.
 struct TreeLayout {
-    size_t cuts, ml_part, o_part, total;
+    size_t cuts, arrivals, ml_part, o_part, total;
 };
 
 TreeLayout tree_layout(int head_dim) {
     const size_t rows = 2 * 128 * static_cast<size_t>(pkv::kTreeMaxCtas);
     TreeLayout w;
     w.cuts = pkv::kWorkspaceHeaderBytes;
-    w.ml_part = w.cuts + pkv::kTreeMaxCtas * sizeof(int4);
+    w.arrivals = w.cuts + pkv::kTreeMaxCtas * sizeof(int4);
+    w.ml_part = w.arrivals + pkv::kTreeMaxCtas * sizeof(unsigned);
     w.o_part = w.ml_part + rows * sizeof(float2);
     w.total = w.o_part + rows * head_dim * sizeof(float);
     return w;
@@ -821,28 +822,33 @@ int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const voi
     const TreeLayout lay = tree_layout(head_dim);
     char *ws = static_cast<char *>(workspace);
     a.cuts = reinterpret_cast<int4 *>(ws + lay.cuts);
+    a.arrivals = reinterpret_cast<unsigned *>(ws + lay.arrivals);
     a.ml_part = reinterpret_cast<float2 *>(ws + lay.ml_part);
     a.o_part = reinterpret_cast<float *>(ws + lay.o_part);
     const int sms = sm_count();
     if (sms <= 0) return fail(PKV_ERR_CUDA, "no current device");
     a.tile_drafts = 128 / group;
-    const int tiles = max_query_len > a.tile_drafts ? 2 : 1;
-    a.group_drafts = tiles * a.tile_drafts;
+    a.lists = max_query_len > a.tile_drafts ? 2 : 1;
     a.piece_cost = 2;
-    a.min_weight = 4;
     const int64_t most_it = (static_cast<int64_t>(max_blocks_per_seq) * block_size + 63) / 64;
     a.whole = most_it <= 8;
-    const int groups = (max_query_len + a.group_drafts - 1) / a.group_drafts;
-    for (int s0 = 0; s0 < num_seqs; s0 += pkv::kTreeMaxSeqs) {
-        a.num_seqs = num_seqs - s0 < pkv::kTreeMaxSeqs ? num_seqs - s0 : pkv::kTreeMaxSeqs;
+    a.min_weight = a.whole ? 1 : 4;
+    // A launch's weights are 32-bit sums: at most so many sequences as cannot pass them.
+    const int64_t tiles = (max_query_len + a.tile_drafts - 1) / a.tile_drafts;
+    const int64_t per_seq = num_kv_heads * tiles * (most_it + a.piece_cost);
+    if (per_seq > 0x7fffffff) return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq %d is too long for %lld heads and "
+                                          "row tiles", max_blocks_per_seq, static_cast<long long>(num_kv_heads * tiles));
+    const int64_t fit = 0x7fffffff / per_seq;
+    const int chunk = static_cast<int>(fit < pkv::kTreeMaxSeqs ? fit : pkv::kTreeMaxSeqs);
+    for (int s0 = 0; s0 < num_seqs; s0 += chunk) {
+        a.num_seqs = num_seqs - s0 < chunk ? num_seqs - s0 : chunk;
         a.block_tables = block_tables + static_cast<int64_t>(s0) * max_blocks_per_seq;
         a.context_lens = context_lens + s0;
         a.query_start = query_start + s0;
         // one wave of CTAs, or fewer where the tables bound the work
-        const int64_t segments = static_cast<int64_t>(a.num_seqs) * num_kv_heads * groups;
-        const int64_t bound = a.whole ? segments : segments * (most_it + a.piece_cost) / a.min_weight + 1;
-        int64_t ctas = static_cast<int64_t>(sms) * (tiles == 1 ? 2 : 1);
-        if (ctas > pkv::kTreeMaxCtas / tiles) ctas = pkv::kTreeMaxCtas / tiles;
+        const int64_t bound = a.whole ? a.num_seqs * num_kv_heads * tiles : a.num_seqs * per_seq / a.min_weight + 1;
+        int64_t ctas = 2 * static_cast<int64_t>(sms);
+        if (ctas > pkv::kTreeMaxCtas) ctas = pkv::kTreeMaxCtas;
         if (ctas > bound) ctas = bound;
         const cudaError_t e = pkv::tree_launch(head_dim, tm_q, tm_k, tm_v, a, static_cast<int>(ctas),
                                                static_cast<cudaStream_t>(stream));

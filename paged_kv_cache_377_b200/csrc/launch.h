@@ -78,17 +78,18 @@ struct TreeArgs {
         max_blocks_per_seq, num_blocks;
     float scale_log2;             // not zero
     int tile_drafts;              // drafts of a 128-row tile: 128 / group
-    int group_drafts;             // drafts that share a pass over K and V: one tile's or two tiles'
+    int lists;                    // 2: some sequence may take a second row tile
     int piece_cost;               // a segment's fixed weight, in iterations
     int min_weight;               // iterations that make another CTA worth it
     int whole;                    // 1: no segment is cut
-    float *o_part;                // fp32 [2 * CTAs][rows][D]: each CTA's partials of a continued and of a begun segment
+    float *o_part;                // fp32 [2 * CTAs][D / 4][128][4]: a CTA's partials of a continued and of a begun segment
     float2 *ml_part;              // their rows' maximum (log2 domain) and sum
-    int4 *cuts;                   // [CTAs]: the cut segment that a CTA begins (see tree_merge_kernel)
+    int4 *cuts;                   // [CTAs]: the segment of over two pieces that a CTA begins (see tree_merge_kernel)
+    unsigned *arrivals;           // [CTAs]: pieces stored of a two-piece segment, by first CTA; 0 between launches
 };
 
 constexpr int kTreeMaxSeqs = 1024;  // sequences of one launch (weights kept in shared memory)
-constexpr int kTreeMaxCtas = 320;   // one-tile CTAs; half as many of two tiles
+constexpr int kTreeMaxCtas = 320;
 
 cudaError_t tree_launch(int head_dim, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                         const TreeArgs &args, int ctas, cudaStream_t stream);

@@ -152,6 +152,7 @@ __device__ __forceinline__ void umma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64
 // A bounded wait whose outcome is the same for the whole warp (tensor-memory
 // loads and stores that follow are warp-collective).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const bool got = mbar_wait_bounded(bar, parity, abort, status);
     return __all_sync(0xffffffffu, got);
 }

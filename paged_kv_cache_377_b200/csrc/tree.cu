@@ -6,21 +6,24 @@
 // what it sees, zero where it sees nothing.
 //
 // A row is a (draft, query head of the kv head's group) pair: 128 / G drafts
-// make a row tile, and one pass over a sequence's K and V serves a row group
-// of TILES row tiles (1: two CTAs per SM; 2, for trees of more rows: one CTA
-// per SM). Sequences, kv heads and row groups make segments of 64-token
-// iterations; the CTAs of one wave take equal shares of all iterations (plus a
-// fixed cost per segment), so a long context is cut between many CTAs and short
-// ones are strung together in one. A cut segment leaves fp32 partials (O, the
-// maximum and the sum of each row), which tree_merge_kernel joins.
+// make a row tile. Sequences, kv heads and row tiles make segments of 64-token
+// iterations; the CTAs of one wave (two per SM) take equal shares of all
+// iterations, plus a fixed cost per segment, so a long context is cut between
+// many CTAs and short ones are strung together in one. The even row tiles of
+// all sequences come first, then the odd ones: where a batch's trees take two
+// tiles, the CTAs c and c + C / 2 walk the same K and V at the same time, and
+// the second read is an L2 hit.
+// A segment cut in two is joined by whichever of its CTAs comes second; one cut
+// in more leaves fp32 partials (O, the maximum and the sum of each row) to
+// tree_merge_kernel.
 //
 // Roles, each walking the CTA's share on its own: one warp brings Q and K by
-// TMA, one V, one per row tile issues its MMAs (S = Q K^T into tensor memory, O +=
-// P V with P read from there), and four warps per row tile hold a row per thread: they
-// load its 64 logits, hide what the row does not see, keep the running maximum
-// and sum in fp32, and write P in bf16 beside S. The mask only matters in the
-// iterations that reach past the committed tokens: a row's bits for 64 positions
-// are two words there.
+// TMA, one V, one issues the MMAs (S = Q K^T into tensor memory, O += P V with P
+// read from there), and four warps hold a row per thread: they load its 64
+// logits, hide what the row does not see, keep the running maximum and sum in
+// fp32, and write P in bf16 beside S. The mask only matters in the iterations
+// that reach past the committed tokens: a row's bits for 64 positions are two
+// words there.
 #include <cuda_bf16.h>
 
 #include "device_utils.cuh"
@@ -33,42 +36,44 @@ namespace {
 constexpr int kRows = 128;       // rows of a tile (= tensor-memory lanes)
 constexpr int kTokens = 64;      // positions of one iteration
 constexpr int kBadRing = 8;      // iterations whose bad-block bits are kept (a loader is at most 5 ahead)
-constexpr int kPoisonRing = 16;  // pieces whose flag is kept (one tile's warps are at most 6 ahead of the other's)
 
 // A CTA's share of the step, piece by piece (a piece: consecutive iterations of
 // one segment). Every role walks it alike.
 struct Walk {
-    int64_t x, x1;  // weight position, end of the share
-    int s;
-    int q0, n, L, h, i0;  // the piece's sequence, kv head and first draft
+    int x, x1;            // weight position, end of the share
+    int e;                // entry of the weights: sequence e % num_seqs, its even or odd row tiles
+    int s;                // the piece's sequence
+    int q0, n, L, h, i0;  // its queries, length, kv head and first draft
     int nit, it0, it1;    // iterations of its segment, and of the piece
     int it;
 
-    __device__ __forceinline__ bool next_piece(const TreeArgs &a, const int64_t *wp) {
+    __device__ __forceinline__ bool next_piece(const TreeArgs &a, const int *wp) {
         while (x < x1) {
-            while (wp[s + 1] <= x) ++s;
+            while (wp[e + 1] <= x) ++e;
+            const bool odd = e >= a.num_seqs;
+            s = odd ? e - a.num_seqs : e;
             q0 = __ldg(a.query_start + s);
             n = __ldg(a.query_start + s + 1) - q0;
             L = __ldg(a.context_lens + s);
             nit = (L + kTokens - 1) / kTokens;
-            const int64_t w = nit + a.piece_cost, local = x - wp[s], seg = local / w;
-            const int off = static_cast<int>(local - seg * w);
-            int end = static_cast<int>(w);
+            const int w = nit + a.piece_cost, local = x - wp[e], seg = local / w, off = local - seg * w;
+            int end = w;
             if (a.whole) {
                 if (off > 0) {  // the segment began in another CTA's share
                     x += w - off;
                     continue;
                 }
             } else if (w - off > x1 - x) {
-                end = off + static_cast<int>(x1 - x);
+                end = off + (x1 - x);
             }
             x += end - off;
             it0 = max(0, off - a.piece_cost);
             it1 = max(0, end - a.piece_cost);
             if (it1 > it0) {
-                const int groups = (n + a.group_drafts - 1) / a.group_drafts;
-                h = static_cast<int>(seg / groups);
-                i0 = static_cast<int>(seg % groups) * a.group_drafts;
+                const int tiles = (n + a.tile_drafts - 1) / a.tile_drafts;
+                const int mine = (tiles + (odd ? 0 : 1)) >> 1;  // even or odd tiles of the sequence
+                h = seg / mine;
+                i0 = (2 * (seg - h * mine) + (odd ? 1 : 0)) * a.tile_drafts;
                 it = it0;
                 return true;
             }
@@ -76,19 +81,12 @@ struct Walk {
         return false;
     }
     // The next iteration (of this piece or the next one).
-    __device__ __forceinline__ bool next(const TreeArgs &a, const int64_t *wp) {
-        return ++it < it1 || next_piece(a, wp);
-    }
-    // Row tiles with a live row.
-    __device__ __forceinline__ int tiles(const TreeArgs &a) const {
-        return min(a.group_drafts, n - i0) > a.tile_drafts ? 2 : 1;
-    }
+    __device__ __forceinline__ bool next(const TreeArgs &a, const int *wp) { return ++it < it1 || next_piece(a, wp); }
 };
 
-// The 64 visibility bits of a mask row (n drafts, committed positions before
-// them) for positions t0 .. t0 + 63; t0 is below the context's end and t0 + 63
-// at or past its first draft.
-__device__ __forceinline__ uint64_t visible_bits(const int32_t *row, int n, int first, int t0) {
+// The 64 visibility bits of a mask row (n drafts behind `first` committed positions) for positions t0 .. t0 + 63,
+// where t0 + 63 is at or past the first draft.
+__device__ __forceinline__ uint2 visible_bits(const int32_t *row, int n, int first, int t0) {
     const int j0 = t0 - first;  // draft of bit 0 (negative: committed positions before)
     const int w0 = max(j0, 0) >> 5, words = (n + 31) >> 5;
     uint32_t w[3];
@@ -98,13 +96,11 @@ __device__ __forceinline__ uint64_t visible_bits(const int32_t *row, int n, int 
         const int left = n - 32 * (w0 + k);  // drafts from this word on
         if (left < 32) w[k] = left > 0 ? w[k] & ((1u << left) - 1u) : 0u;
     }
-    if (j0 >= 0) {
-        const int sh = j0 & 31;
-        const uint32_t lo = __funnelshift_r(w[0], w[1], sh), hi = __funnelshift_r(w[1], w[2], sh);
-        return (static_cast<uint64_t>(hi) << 32) | lo;
-    }
+    if (j0 >= 0)
+        return make_uint2(__funnelshift_r(w[0], w[1], j0 & 31), __funnelshift_r(w[1], w[2], j0 & 31));
     const uint64_t bits = (static_cast<uint64_t>(w[1]) << 32) | w[0];
-    return j0 <= -64 ? ~0ull : (bits << -j0) | ((1ull << -j0) - 1ull);
+    const uint64_t vis = (bits << -j0) | ((1ull << -j0) - 1ull);
+    return make_uint2(static_cast<uint32_t>(vis), static_cast<uint32_t>(vis >> 32));
 }
 
 template <int D>
@@ -116,90 +112,108 @@ struct TreeShape {
     static constexpr uint32_t kTileQ = HALVES * kQHalf;
 };
 
-constexpr int tree_stages(int tiles) { return tiles == 1 ? 2 : 4; }
-constexpr int tree_threads(int tiles) { return tiles * 160 + 64; }
+constexpr int kStages = 2;
+constexpr int kSoftmaxWarps = 4, kLoadK = 4, kLoadV = 5, kMma = 6;
+constexpr int kThreads = 224;
+constexpr uint32_t kTmemCols = 256;  // S | two buffers of P | O: two CTAs fill an SM's 512
 
 struct TreeBars {
-    uint64_t q_full, q_empty, done[2];
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-    // per tile: S is in tensor memory; the softmax threads have loaded it; P (buffer b) is written; O += P V
-    // of buffer b is done; the piece's O is done
-    uint64_t s_full[2], s_free[2], p_ready[2][2], pv_free[2][2], o_full[2];
-    int64_t scan[16];
+    uint64_t q_full, q_empty, done;
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    // S is in tensor memory; the softmax threads have loaded it; P (buffer b) is written; O += P V of buffer b is
+    // done; the piece's O is done
+    uint64_t s_full, s_free, p_ready[2], pv_free[2], o_full;
+    uint64_t all;  // the softmax warps meet
+    int scan[16];
     uint32_t bad[kBadRing];
     uint32_t tmem;
     int abort;
-    int poison[kPoisonRing];
+    int arrived;
+    int poison[2];
 };
 
-template <int D, int BS, int TILES>
-__global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
+template <int D, int BS>
+__global__ void __launch_bounds__(kThreads, 2)
     paged_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
     using Sh = TreeShape<D>;
-    constexpr int HALVES = Sh::HALVES, BPI = kTokens / BS, STAGES = tree_stages(TILES);
-    constexpr int kThreads = tree_threads(TILES), kLoadK = 4 * TILES, kLoadV = kLoadK + 1, kMma = kLoadK + 2;
-    constexpr uint32_t kTmemCols = 256 * TILES;
+    constexpr int HALVES = Sh::HALVES, BPI = kTokens / BS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // ---- shared memory: Q tiles | K stages | V stages | barriers | weights before each sequence
+    // ---- shared memory: Q | K stages | V stages | barriers | weights before each entry
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sq = base;
-    uint8_t *sk = sq + TILES * Sh::kTileQ;
-    uint8_t *sv = sk + STAGES * Sh::kTileKV;
-    TreeBars &B = *reinterpret_cast<TreeBars *>(sv + STAGES * Sh::kTileKV);
-    int64_t *wp = reinterpret_cast<int64_t *>(&B + 1);
+    uint8_t *sk = sq + Sh::kTileQ;
+    uint8_t *sv = sk + kStages * Sh::kTileKV;
+    TreeBars &B = *reinterpret_cast<TreeBars *>(sv + kStages * Sh::kTileKV);
+    int *wp = reinterpret_cast<int *>(&B + 1);
 
     // ---- weights: every CTA sums over all sequences (one contiguous run per thread)
+    const int entries = a.num_seqs * a.lists;
     {
         const int per = (a.num_seqs + kThreads - 1) / kThreads;
         const int s0 = min(tid * per, a.num_seqs), s1 = min(s0 + per, a.num_seqs);
-        int64_t sum = 0;
+        int sum[2] = {0, 0};
         for (int s = s0; s < s1; ++s) {
             const int q0 = __ldg(a.query_start + s), n = __ldg(a.query_start + s + 1) - q0;
             const int L = __ldg(a.context_lens + s);
-            int64_t w = 0;
+            int tiles = 0;
             if (q0 < 0 || n < 0 || q0 > a.num_tokens - n || n > a.max_query_len || n > L ||
                 L > static_cast<int64_t>(a.max_blocks_per_seq) * BS) {
                 if (blockIdx.x == 0) atomicOr(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
-            } else if (n > 0) {
-                w = static_cast<int64_t>(a.num_kv_heads) * ((n + a.group_drafts - 1) / a.group_drafts) *
-                    ((L + kTokens - 1) / kTokens + a.piece_cost);
+            } else {
+                tiles = (n + a.tile_drafts - 1) / a.tile_drafts;
             }
-            wp[s + 1] = w;
-            sum += w;
+            const int w = a.num_kv_heads * ((L + kTokens - 1) / kTokens + a.piece_cost);
+            for (int k = 0; k < a.lists; ++k) {
+                const int mine = tiles > 0 ? w * ((tiles + 1 - k) >> 1) : 0;
+                wp[k * a.num_seqs + s + 1] = mine;
+                sum[k] += mine;
+            }
         }
-        int64_t inc = sum;
+        int inc[2] = {sum[0], sum[1]};
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += y;
+            const int y0 = __shfl_up_sync(0xffffffffu, inc[0], d), y1 = __shfl_up_sync(0xffffffffu, inc[1], d);
+            if (lane >= d) {
+                inc[0] += y0;
+                inc[1] += y1;
+            }
         }
-        if (lane == 31) B.scan[warp] = inc;
+        if (lane == 31) {
+            B.scan[warp] = inc[0];
+            B.scan[8 + warp] = inc[1];
+        }
         __syncthreads();
-        int64_t run = inc - sum;
-        for (int w = 0; w < warp; ++w) run += B.scan[w];
-        for (int s = s0; s < s1; ++s) {
-            run += wp[s + 1];
-            wp[s + 1] = run;
+        int run[2] = {inc[0] - sum[0], inc[1] - sum[1]};
+        for (int w = 0; w < kThreads / 32; ++w) {
+            run[1] += B.scan[w];  // the odd tiles come behind all even ones
+            if (w < warp) {
+                run[0] += B.scan[w];
+                run[1] += B.scan[8 + w];
+            }
         }
+        for (int k = 0; k < a.lists; ++k)
+            for (int s = s0; s < s1; ++s) {
+                run[k] += wp[k * a.num_seqs + s + 1];
+                wp[k * a.num_seqs + s + 1] = run[k];
+            }
         if (tid == 0) {
             wp[0] = 0;
             if (!a.whole) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
         }
     }
     __syncthreads();
-    const int64_t W = wp[a.num_seqs];
-    const int64_t most = (W + a.min_weight - 1) / a.min_weight;
-    const int C = static_cast<int>(most < gridDim.x ? most : gridDim.x);  // CTAs that take a share
+    const int W = wp[entries];
+    const int C = min(static_cast<int>(gridDim.x), W / a.min_weight + (W % a.min_weight != 0));  // CTAs that take a share
     const int c = blockIdx.x;
     if (c >= C) return;
     Walk walk;
-    walk.x = W * c / C;
-    walk.x1 = W * (c + 1) / C;
+    walk.x = static_cast<int>(static_cast<int64_t>(W) * c / C);
+    walk.x1 = static_cast<int>(static_cast<int64_t>(W) * (c + 1) / C);
     {
-        int lo = 0, hi = a.num_seqs;  // wp[lo] <= x < wp[hi]
+        int lo = 0, hi = entries;  // wp[lo] <= x < wp[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (wp[mid] <= walk.x)
@@ -207,7 +221,7 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
             else
                 hi = mid;
         }
-        walk.s = lo;
+        walk.e = lo;
     }
 
     if (warp == kMma) {  // all of the CTA's columns
@@ -217,24 +231,23 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
         tc_fence_before();
     } else if (warp == kLoadK && lane == 0) {
         mbar_init(&B.q_full, 1);
-        mbar_init(&B.q_empty, TILES);
-        for (int i = 0; i < STAGES; ++i) {
+        mbar_init(&B.q_empty, 1);
+        mbar_init(&B.done, 1);
+        mbar_init(&B.s_full, 1);
+        mbar_init(&B.s_free, kSoftmaxWarps);
+        mbar_init(&B.o_full, 1);
+        mbar_init(&B.all, kSoftmaxWarps);
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&B.k_full[i], 1);
-            mbar_init(&B.k_empty[i], TILES);
+            mbar_init(&B.k_empty[i], 1);
             mbar_init(&B.v_full[i], 1);
-            mbar_init(&B.v_empty[i], TILES);
+            mbar_init(&B.v_empty[i], 1);
         }
-        for (int t = 0; t < TILES; ++t) {
-            mbar_init(&B.done[t], 1);
-            mbar_init(&B.s_full[t], 1);
-            mbar_init(&B.s_free[t], 128);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&B.p_ready[t][i], 128);
-                mbar_init(&B.pv_free[t][i], 1);
-            }
-            mbar_init(&B.o_full[t], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.p_ready[i], kSoftmaxWarps);
+            mbar_init(&B.pv_free[i], 1);
+            B.poison[i] = 0;
         }
-        for (int i = 0; i < kPoisonRing; ++i) B.poison[i] = 0;
         B.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -265,8 +278,8 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
             Walk ahead = walk;
             const bool more2 = ahead.next(a, wp);
             const int p2 = more2 ? entry(ahead) : -1;  // in flight while this iteration waits
-            const int st = g % STAGES;
-            if (g >= STAGES && !(ok = warp_wait(&empty[st], (g / STAGES - 1) & 1u, abort_flag, a.status))) break;
+            const int st = g % kStages;
+            if (g >= kStages && !(ok = warp_wait(&empty[st], (g / kStages - 1) & 1u, abort_flag, a.status))) break;
             const bool there = lane < BPI * HALVES && (walk.it * BPI + jb) * BS < walk.L;
             const bool mine = there && p >= 0 && p < a.num_blocks;
             const unsigned m = __ballot_sync(0xffffffffu, mine), lost = __ballot_sync(0xffffffffu, there && !mine);
@@ -285,13 +298,10 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                 // the piece's queries, once the MMAs of the piece before are done with theirs
                 if (pieces > 0 && !(ok = warp_wait(&B.q_empty, (pieces - 1) & 1u, abort_flag, a.status))) break;
                 if (lane == 0) {
-                    const int tiles = TILES == 1 ? 1 : walk.tiles(a);
-                    mbar_arrive_expect_tx(&B.q_full, tiles * HALVES * a.tile_drafts * a.group * 128);
-                    for (int t = 0; t < tiles; ++t)
+                    mbar_arrive_expect_tx(&B.q_full, HALVES * a.tile_drafts * a.group * 128);
 #pragma unroll
-                        for (int q = 0; q < HALVES; ++q)
-                            tma_load_5d(sq + t * Sh::kTileQ + q * Sh::kQHalf, &tm_q, &B.q_full, 0, q, 0, walk.h,
-                                        walk.q0 + walk.i0 + t * a.tile_drafts);
+                    for (int q = 0; q < HALVES; ++q)
+                        tma_load_5d(sq + q * Sh::kQHalf, &tm_q, &B.q_full, 0, q, 0, walk.h, walk.q0 + walk.i0);
                 }
                 __syncwarp();
                 q_issued = true;
@@ -305,71 +315,58 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
         // copies still in flight (only after a wait gave up) land before exit
         if (!ok || *abort_flag) {
             if (q_issued) mbar_wait_drain(&B.q_full, (pieces - 1) & 1u, a.status);
-            for (uint32_t u = g > STAGES ? g - STAGES : 0; u < g; ++u)
-                mbar_wait_drain(&full[u % STAGES], (u / STAGES) & 1u, a.status);
+            for (uint32_t u = g > kStages ? g - kStages : 0; u < g; ++u)
+                mbar_wait_drain(&full[u % kStages], (u / kStages) & 1u, a.status);
         }
         __syncwarp();
-    } else if (warp >= kMma) {
-        // ---------------- MMA warp of tile t: one elected lane issues. S(it + 1) is issued as soon as the softmax
-        // warps hold S(it) in registers, and runs while they work on it; O += P(it) V(it) follows P(it).
-        const int t = TILES == 1 ? 0 : warp - kMma;
+    } else if (warp == kMma) {
+        // ---------------- MMA warp: one elected lane issues. S(it + 1) is issued as soon as the softmax warps hold
+        // S(it) in registers, and runs while they work on it; O += P(it) V(it) follows P(it).
         const bool leader = elect_one();
-        const uint64_t dq = smem_desc(smem_u32(sq + t * Sh::kTileQ), 16, 1024), dk = smem_desc(smem_u32(sk), 16, 1024),
+        const uint64_t dq = smem_desc(smem_u32(sq), 16, 1024), dk = smem_desc(smem_u32(sk), 16, 1024),
                        dv = smem_desc(smem_u32(sv), Sh::kHalfKV, 1024);
-        const uint32_t t_s = tbase + 256 * t, t_p = t_s + 64, t_o = t_s + 128;
+        const uint32_t t_p = tbase + 64, t_o = tbase + 128;
         Walk ws = walk, wv = walk;
-        uint32_t gs = 0, gv = 0, pieces = 0, us = 0, uv = 0;  // iterations, pieces; iterations with a live tile
+        uint32_t gs = 0, gv = 0, pieces = 0;
         bool ok = true;
         auto step_s = [&]() {
-            const int st = gs % STAGES;
-            const bool last = ws.it + 1 == ws.it1, live = t < ws.tiles(a);
+            const int st = gs % kStages;
             if (ws.it == ws.it0) {
                 if (!(ok = warp_wait(&B.q_full, pieces & 1u, abort_flag, a.status))) return;
                 ++pieces;
             }
-            if (!(ok = warp_wait(&B.k_full[st], (gs / STAGES) & 1u, abort_flag, a.status))) return;
-            if (live) {
-                if (us > 0 && !(ok = warp_wait(&B.s_free[t], (us - 1) & 1u, abort_flag, a.status))) return;
-                tc_fence_after();
-                if (leader) {
+            if (!(ok = warp_wait(&B.k_full[st], (gs / kStages) & 1u, abort_flag, a.status))) return;
+            if (gs > 0 && !(ok = warp_wait(&B.s_free, (gs - 1) & 1u, abort_flag, a.status))) return;
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
-                    for (int hf = 0; hf < HALVES; ++hf)
+                for (int hf = 0; hf < HALVES; ++hf)
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma(t_s, dq + ((hf * Sh::kQHalf + kk * 32) >> 4),
-                                 dk + ((st * Sh::kTileKV + hf * Sh::kHalfKV + kk * 32) >> 4),
-                                 instr_desc(128, kTokens, false), (hf | kk) != 0);
-                    umma_commit(&B.s_full[t]);
-                    umma_commit(&B.k_empty[st]);
-                    if (last) umma_commit(&B.q_empty);
-                }
-                ++us;
-            } else if (lane == 0) {
-                mbar_arrive(&B.k_empty[st]);
-                if (last) mbar_arrive(&B.q_empty);
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma(tbase, dq + ((hf * Sh::kQHalf + kk * 32) >> 4),
+                             dk + ((st * Sh::kTileKV + hf * Sh::kHalfKV + kk * 32) >> 4),
+                             instr_desc(128, kTokens, false), (hf | kk) != 0);
+                umma_commit(&B.s_full);
+                umma_commit(&B.k_empty[st]);
+                if (ws.it + 1 == ws.it1) umma_commit(&B.q_empty);
             }
             __syncwarp();
             ++gs;
         };
         auto step_v = [&]() {
-            const int st = gv % STAGES;
-            const uint32_t b = uv & 1u;
-            if (!(ok = warp_wait(&B.v_full[st], (gv / STAGES) & 1u, abort_flag, a.status))) return;
-            if (t < wv.tiles(a)) {
-                if (!(ok = warp_wait(&B.p_ready[t][b], (uv >> 1) & 1u, abort_flag, a.status))) return;
-                tc_fence_after();
-                if (leader) {
+            const int st = gv % kStages;
+            const uint32_t b = gv & 1u;
+            if (!(ok = warp_wait(&B.v_full[st], (gv / kStages) & 1u, abort_flag, a.status))) return;
+            if (!(ok = warp_wait(&B.p_ready[b], (gv >> 1) & 1u, abort_flag, a.status))) return;
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_ts(t_o, t_p + 32 * b + kk * 8, dv + ((st * Sh::kTileKV + kk * 16 * 128) >> 4),
-                                instr_desc(128, D, true), wv.it != wv.it0 || kk != 0);
-                    umma_commit(&B.pv_free[t][b]);
-                    umma_commit(&B.v_empty[st]);
-                    if (wv.it + 1 == wv.it1) umma_commit(&B.o_full[t]);
-                }
-                ++uv;
-            } else if (lane == 0) {
-                mbar_arrive(&B.v_empty[st]);
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_ts(t_o, t_p + 32 * b + kk * 8, dv + ((st * Sh::kTileKV + kk * 16 * 128) >> 4),
+                            instr_desc(128, D, true), wv.it != wv.it0 || kk != 0);
+                umma_commit(&B.pv_free[b]);
+                umma_commit(&B.v_empty[st]);
+                if (wv.it + 1 == wv.it1) umma_commit(&B.o_full);
             }
             __syncwarp();
             ++gv;
@@ -390,62 +387,71 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
             more_v = wv.next(a, wp);
         }
         // every MMA issued is done before the tensor memory is freed (one phase: nothing aliases)
-        if (leader) umma_commit(&B.done[t]);
+        if (leader) umma_commit(&B.done);
         __syncwarp();
-        mbar_wait_drain(&B.done[t], 0, a.status);
+        mbar_wait_drain(&B.done, 0, a.status);
         __syncwarp();
     } else {
-        // ---------------- softmax warps: thread r of tile t owns a row (tensor-memory lane r)
-        const int t = TILES == 1 ? 0 : warp >> 2, r = tid & 127, wlane = (warp & 3) * 32;
-        const uint32_t t_s = tbase + 256 * t + (static_cast<uint32_t>(wlane) << 16), t_p = t_s + 64, t_o = t_s + 128;
-        const int G = a.group, row_draft = t * a.tile_drafts + r / G;  // draft of this row within the row group
+        // ---------------- softmax warps: thread r owns row r (tensor-memory lane r)
+        const int r = tid;
+        const uint32_t t_s = tbase + (static_cast<uint32_t>(warp * 32) << 16), t_p = t_s + 64, t_o = t_s + 128;
+        const int G = a.group;
         const float c2 = fabsf(a.scale_log2);
         const bool negative = a.scale_log2 < 0.f, spare = r >= a.tile_drafts * G;
         volatile int *poison = B.poison;
-        uint32_t u = 0, g = 0, mine = 0, pieces = 0;
+        uint32_t g = 0, pieces = 0, met_all = 0;
         bool ok = true;
+        auto signal = [&](uint64_t *bar) {  // one arrival per warp, after all its lanes
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        auto meet_all = [&]() {
+            signal(&B.all);
+            return ok = warp_wait(&B.all, met_all++ & 1u, abort_flag, a.status);
+        };
         while (ok && walk.next_piece(a, wp)) {
             const uint32_t piece = pieces++;
-            if (t >= walk.tiles(a)) {  // no live row in this tile
-                g += walk.it1 - walk.it0;
-                continue;
-            }
-            const int draft = walk.i0 + row_draft;
-            const bool live = !spare && row_draft < a.group_drafts && draft < walk.n;
+            const int draft = walk.i0 + r / G;
+            const bool live = !spare && draft < walk.n;
             const bool warp_live = __any_sync(0xffffffffu, live);
             const int first = walk.L - walk.n;  // first draft's position
             const int32_t *bits = a.tree_mask + static_cast<int64_t>(walk.q0 + min(draft, walk.n - 1)) * a.mask_words;
             float m_ref = -INFINITY, l_run = 0.f;
-            for (int it = walk.it0; it < walk.it1; ++it, ++u, ++g) {
-                const uint32_t b = u & 1u;
+            for (int it = walk.it0; it < walk.it1; ++it, ++g) {
+                const uint32_t b = g & 1u;
                 const int t0 = it * kTokens;
-                if (!(ok = warp_wait(&B.s_full[t], u & 1u, abort_flag, a.status))) break;
+                if (!(ok = warp_wait(&B.s_full, g & 1u, abort_flag, a.status))) break;
                 const uint32_t bad = B.bad[g % kBadRing];
                 const bool tail = t0 + kTokens > first;
                 if (!warp_live) {
-                    mbar_arrive(&B.s_free[t]);
+                    signal(&B.s_free);
                 } else {
                     tc_fence_after();
                     float x[64];
                     tmem_ld64(t_s, x);
                     tc_fence_before();
-                    mbar_arrive(&B.s_free[t]);
+                    signal(&B.s_free);
                     if (negative) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i) x[i] = -x[i];
                     }
                     if (tail || bad) {
-                        uint64_t vis = tail ? visible_bits(bits, walk.n, first, t0) : ~0ull;
+                        uint2 vis = tail ? visible_bits(bits, walk.n, first, t0) : make_uint2(~0u, ~0u);
                         if (bad) {
 #pragma unroll
-                            for (int k = 0; k < BPI; ++k)
-                                if ((bad >> (k * HALVES)) & 1u) vis &= ~(((1ull << BS) - 1ull) << (k * BS));
+                            for (int k = 0; k < BPI; ++k) {
+                                if (!((bad >> (k * HALVES)) & 1u)) continue;
+                                const uint32_t gone = BS == 32 ? ~0u : 0xffffu << (k % 2 * 16);
+                                if (k * BS < 32)
+                                    vis.x &= ~gone;
+                                else
+                                    vis.y &= ~gone;
+                            }
                         }
-                        const uint32_t lo = static_cast<uint32_t>(vis), hi = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            if (!((lo >> i) & 1u)) x[i] = -INFINITY;
-                            if (!((hi >> i) & 1u)) x[32 + i] = -INFINITY;
+                            if (!((vis.x >> i) & 1u)) x[i] = -INFINITY;
+                            if (!((vis.y >> i) & 1u)) x[32 + i] = -INFINITY;
                         }
                     }
                     float mx;
@@ -464,17 +470,17 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                     float m_new = m_ref;
                     if (mx * c2 > m_ref + 8.f) m_new = mx * c2;
                     const float alpha = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+                    const bool moved = it > walk.it0 && __any_sync(0xffffffffu, alpha != 1.f);
                     const float shift = m_new == -INFINITY ? 0.f : -m_new;  // a row that has seen nothing: P = 0
                     const float2 cc = make_float2(c2, c2), nm = make_float2(shift, shift);
                     float2 ps2a = make_float2(0.f, 0.f), ps2b = make_float2(0.f, 0.f);
-                    if (u >= 2 && !(ok = warp_wait(&B.pv_free[t][b], ((u >> 1) - 1) & 1u, abort_flag, a.status))) break;
-                    tc_fence_after();
+                    // P's buffer is free: S(it) was committed behind the P V before last
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    for (int part = 0; part < 2; ++part) {
                         uint32_t w[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int i = 32 * half + 2 * e;
+                            const int i = 32 * part + 2 * e;
                             const float2 arg = ffma2(make_float2(x[i], x[i + 1]), cc, nm);
                             const float2 pr = make_float2(fast_exp2(arg.x), fast_exp2(arg.y));
                             if (e & 1)
@@ -484,16 +490,15 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                             const __nv_bfloat162 v2 = __floats2bfloat162_rn(pr.x, pr.y);
                             w[e] = *reinterpret_cast<const uint32_t *>(&v2);
                         }
-                        tmem_st16(t_p + 32 * b + 16 * half, w);
+                        tmem_st16(t_p + 32 * b + 16 * part, w);
                     }
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     l_run = l_run * alpha + ((ps2a.x + ps2b.x) + (ps2a.y + ps2b.y));
                     m_ref = m_new;
                     // rescale O where the reference moved, once O += P(it - 1) V(it - 1) is done
-                    if (it > walk.it0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        if (!(ok = warp_wait(&B.pv_free[t][b ^ 1u], ((u - 1) >> 1) & 1u, abort_flag, a.status))) break;
+                    if (moved) {
+                        if (!(ok = warp_wait(&B.pv_free[b ^ 1u], ((g - 1) >> 1) & 1u, abort_flag, a.status))) break;
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int cb = 0; cb < D / 32; ++cb) {
                             float o[32];
                             tmem_ld32(t_o + cb * 32, o);
@@ -502,14 +507,14 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                             tmem_st32(t_o + cb * 32, o);
                         }
                     }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
                 // V rows that hold no token (past the context, or of a bad block) may be anything: zero, so that
                 // P = 0 there multiplies zeros. A draft's V that is not finite is hidden from the rows that do not
-                // see it in the same way, and added back to the others at the end. Each tile's warps do so before
-                // their own P V; both write the same bytes, the flag always before the first of them.
+                // see it in the same way, and added back to the others at the end.
                 if (tail || bad) {
-                    const int st = g % STAGES;
-                    if (!(ok = warp_wait(&B.v_full[st], (g / STAGES) & 1u, abort_flag, a.status))) break;
+                    const int st = g % kStages;
+                    if (!(ok = warp_wait(&B.v_full[st], (g / kStages) & 1u, abort_flag, a.status))) break;
                     uint8_t *vt = sv + st * Sh::kTileKV;
                     for (int e = r; e < HALVES * kTokens * 8; e += 128) {
                         const int hf = e / (kTokens * 8), tok = (e / 8) % kTokens, ch = e % 8;
@@ -532,84 +537,136 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
                                 }
                             }
                             if (any) {
-                                poison[piece % kPoisonRing] = 1;
-                                __threadfence_block();
+                                poison[piece & 1u] = 1;
                                 *at = v;
                             }
                         }
                     }
-                    __threadfence_block();
                     fence_proxy_async_shared();
                 }
                 tc_fence_before();
-                mbar_arrive(&B.p_ready[t][b]);
+                signal(&B.p_ready[b]);
             }
             if (!ok) break;
-            if (!(ok = warp_wait(&B.o_full[t], mine & 1u, abort_flag, a.status))) break;
-            ++mine;
+            // ---- the piece's end
+            if (!(ok = warp_wait(&B.o_full, piece & 1u, abort_flag, a.status))) break;
             tc_fence_after();
-            if (*abort_flag) break;
-            const bool poisoned = poison[piece % kPoisonRing] != 0;
-            if (t == 0 && r == 0) poison[(piece + kPoisonRing / 2) % kPoisonRing] = 0;
-            const bool cut = walk.it0 > 0 || walk.it1 < walk.nit;
-            const int64_t row = static_cast<int64_t>(c) * 2 + (walk.it0 > 0 ? 0 : 1);  // the CTA's partial
-            float *part = nullptr;
-            __nv_bfloat16 *dst = nullptr;
-            if (cut) {
-                const int64_t pr = row * (TILES * kRows) + t * kRows + r;
-                part = a.o_part + pr * D;
-                if (live) a.ml_part[pr] = make_float2(m_ref, l_run);
-                if (t == 0 && r == 0 && walk.it0 == 0) {
-                    // the segment's first piece: its last iteration's weight position tells how many follow
-                    const int64_t w = walk.nit + a.piece_cost, left = w - (walk.it1 + a.piece_cost);
-                    const int64_t last = walk.x + left - 1;
-                    const int last_cta = static_cast<int>(((last + 1) * C - 1) / W);
-                    a.cuts[c] = make_int4(walk.q0 + walk.i0, walk.n - walk.i0, walk.h, last_cta - c + 1);
-                }
-            } else {
-                dst = static_cast<__nv_bfloat16 *>(a.out) +
-                      (static_cast<int64_t>(walk.q0 + min(draft, walk.n - 1)) * a.num_q_heads + walk.h * G + r % G) * D;
+            const bool poisoned = poison[piece & 1u] != 0;
+            if (poisoned) {  // cleared for the piece after next once all have read it
+                if (!meet_all()) break;
+                if (r == 0) poison[piece & 1u] = 0;
             }
-            const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-            if (warp_live) {
+            // The CTAs whose shares hold the segment's first and last iteration; a whole segment has one.
+            const int64_t at0 = walk.x - walk.it1, at1 = at0 + walk.nit - 1;  // weight positions of those iterations
+            const int cta0 = a.whole ? c : static_cast<int>(((at0 + 1) * C - 1) / W);
+            const int cta1 = a.whole ? c : static_cast<int>(((at1 + 1) * C - 1) / W);
+            auto partial = [&](int cta) { return (cta * 2 + (cta == cta0 ? 1 : 0)) * static_cast<int64_t>(kRows); };
+            bool store = cta1 > cta0, join = false;
+            if (cta1 == cta0 + 1) {
+                // two pieces: whoever comes second joins them from its registers, and nobody waits
+                unsigned *count = a.arrivals + cta0;
+                if (r == 0) {
+                    unsigned seen;
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
+                    B.arrived = static_cast<int>(seen);
+                }
+                if (!meet_all()) break;
+                join = *reinterpret_cast<volatile int *>(&B.arrived) != 0;
+                store = !join;
+            } else if (store && c == cta0 && r == 0) {
+                a.cuts[c] = make_int4(walk.q0 + walk.i0, walk.n - walk.i0, walk.h, cta1 - cta0 + 1);
+            }
+            for (;;) {
+                float scale_mine = l_run == 0.f ? 0.f : 1.f / l_run, scale_other = 0.f;
+                const int64_t own_row = partial(c), other_row = partial(c == cta0 ? cta1 : cta0);
+                if (join) {
+                    const float2 ml = a.ml_part[other_row + r];
+                    const float m = fmaxf(m_ref, ml.x);
+                    const float w0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
+                    const float w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+                    // the same whichever piece comes second: products and sums rounded one by one
+                    const float l = __fadd_rn(__fmul_rn(l_run, w0), __fmul_rn(ml.y, w1));
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    scale_mine = w0 * inv;
+                    scale_other = w1 * inv;
+                } else if (store && live) {
+                    a.ml_part[own_row + r] = make_float2(m_ref, l_run);
+                }
+                if (warp_live) {
+#pragma unroll 1
+                    for (int cb = 0; cb < D / 32; ++cb) {
+                        const int col = cb * 32;
+                        float o[32];
+                        tmem_ld32(t_o + col, o);
+                        if (poisoned && live) {
+                            for (int j = max(walk.it0 * kTokens - first, 0); j < min(walk.it1 * kTokens - first, walk.n);
+                                 ++j) {
+                                if (!((bits[j >> 5] >> (j & 31)) & 1)) continue;
+                                const int pos = first + j;
+                                const int p =
+                                    __ldg(a.block_tables + static_cast<int64_t>(walk.s) * a.max_blocks_per_seq + pos / BS);
+                                if (p < 0 || p >= a.num_blocks) continue;
+                                const __nv_bfloat16 *v =
+                                    static_cast<const __nv_bfloat16 *>(a.v_cache) +
+                                    ((static_cast<int64_t>(p) * BS + pos % BS) * a.num_kv_heads + walk.h) * D + col;
 #pragma unroll
-                for (int cb = 0; cb < D / 32; ++cb) {
-                    float o[32];
-                    tmem_ld32(t_o + cb * 32, o);
-                    if (poisoned && live) {
-                        for (int j = max(walk.it0 * kTokens - first, 0); j < min(walk.it1 * kTokens - first, walk.n); ++j) {
-                            if (!((bits[j >> 5] >> (j & 31)) & 1)) continue;
-                            const int pos = first + j;
-                            const int p = __ldg(a.block_tables + static_cast<int64_t>(walk.s) * a.max_blocks_per_seq + pos / BS);
-                            if (p < 0 || p >= a.num_blocks) continue;
-                            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_cache) +
-                                                     ((static_cast<int64_t>(p) * BS + pos % BS) * a.num_kv_heads + walk.h) * D +
-                                                     cb * 32;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float f = __bfloat162float(v[i]);
-                                if (!isfinite(f)) o[i] += f;
+                                for (int i = 0; i < 32; ++i) {
+                                    const float f = __bfloat162float(v[i]);
+                                    if (!isfinite(f)) o[i] += f;
+                                }
                             }
                         }
-                    }
-                    if (!live) continue;
-                    if (cut) {
+                        if (!live) continue;
+                        // a partial is [columns / 4][rows][4]: a warp's rows are side by side
+                        if (store) {
+                            float4 *part = reinterpret_cast<float4 *>(a.o_part + own_row * D) + (col / 4) * kRows + r;
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(part + cb * 32 + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                    } else {
+                            for (int i = 0; i < 8; ++i)
+                                part[i * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            continue;
+                        }
+                        if (join) {
+                            const float4 *part =
+                                reinterpret_cast<const float4 *>(a.o_part + other_row * D) + (col / 4) * kRows + r;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 v = part[i * kRows];
+                                const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    o[4 * i + k] = __fadd_rn(__fmul_rn(o[4 * i + k], scale_mine), __fmul_rn(e[k], scale_other));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= scale_mine;
+                        }
+                        __nv_bfloat16 *dst =
+                            static_cast<__nv_bfloat16 *>(a.out) +
+                            (static_cast<int64_t>(walk.q0 + draft) * a.num_q_heads + walk.h * G + r % G) * D + col;
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) {
                             uint32_t w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[i + 2 * e] * inv, o[i + 2 * e + 1] * inv);
+                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[i + 2 * e], o[i + 2 * e + 1]);
                                 w[e] = *reinterpret_cast<const uint32_t *>(&v2);
                             }
-                            *reinterpret_cast<uint4 *>(dst + cb * 32 + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     }
                 }
+                if (join || cta1 != cta0 + 1) break;
+                // stored the first of two pieces, or so it seemed: the other may have come meanwhile
+                __threadfence();
+                if (!meet_all()) break;
+                if (r == 0) {
+                    B.arrived = static_cast<int>(atomicAdd(a.arrivals + cta0, 1u));
+                    __threadfence();
+                }
+                if (!meet_all()) break;
+                if (*reinterpret_cast<volatile int *>(&B.arrived) == 0) break;
+                store = false;
+                join = true;
             }
         }
     }
@@ -621,83 +678,71 @@ __global__ void __launch_bounds__(tree_threads(TILES), TILES == 1 ? 2 : 1)
     }
 }
 
-constexpr int kMergeWarps = 8;
+constexpr int kMergeRows = 32;  // rows of a merge CTA: a lane each
+constexpr int kMergeCols = 8;   // warps: a group of D / 8 columns each
 
-// Joins the partials of a cut segment: out = sum_p O_p 2^(m_p - m) / sum_p l_p 2^(m_p - m). One warp per row;
-// blockIdx.x is the CTA that holds the segment's first piece, the following CTAs' first partials are the others.
+// Joins the partials of a segment cut into more than two pieces: out = sum_p O_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).
+// blockIdx.x is the CTA that holds the segment's first piece; the following CTAs' first partials are the others.
+// Also clears the two-piece counters for the next launch.
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kMergeRows * kMergeCols) tree_merge_kernel(const TreeArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.y == 0 && threadIdx.x == 0) a.arrivals[c] = 0;
     const int4 cut = a.cuts[c];  // first row's draft, drafts from there on, kv head, pieces
-    const int k = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-    if (cut.w == 0 || k >= min(cut.y, a.group_drafts) * a.group) return;
-    constexpr int E = D / 32;
-    const int tile_rows = a.tile_drafts * a.group;
-    const int64_t rows = a.group_drafts > a.tile_drafts ? 2 * kRows : kRows;
-    const int64_t at = k / tile_rows * kRows + k % tile_rows;  // the row's place in a partial
-    auto partial = [&](int p) { return (static_cast<int64_t>(c + p) * 2 + (p == 0 ? 1 : 0)) * rows + at; };
+    const int r = blockIdx.y * kMergeRows + lane;
+    if (r >= min(cut.y, a.tile_drafts) * a.group) return;  // no pieces: no drafts
+    auto partial = [&](int p) { return ((c + p) * 2 + (p == 0 ? 1 : 0)) * static_cast<int64_t>(kRows); };
     float m = -INFINITY;
-    for (int p = lane; p < cut.w; p += 32) m = fmaxf(m, a.ml_part[partial(p)].x);
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float o[E] = {}, l = 0.f;
-    for (int p0 = 0; p0 < cut.w; p0 += 32) {
-        const int count = min(32, cut.w - p0);
-        float w = 0.f;
-        if (lane < count) {
-            const float2 ml = a.ml_part[partial(p0 + lane)];
-            w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-            l += ml.y * w;
-        }
 #pragma unroll 4
-        for (int p = 0; p < count; ++p) {
-            const float wp = __shfl_sync(0xffffffffu, w, p);
-            const float *src = a.o_part + partial(p0 + p) * D + lane * E;
-            if (E == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(src);
-                o[0] += v.x * wp;
-                o[1] += v.y * wp;
-                o[E - 2] += v.z * wp;
-                o[E - 1] += v.w * wp;
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(src);
-                o[0] += v.x * wp;
-                o[1] += v.y * wp;
-            }
+    for (int p = 0; p < cut.w; ++p) m = fmaxf(m, a.ml_part[partial(p) + r].x);
+    constexpr int Q = D / 4 / kMergeCols;  // float4 columns per thread
+    float o[4 * Q] = {}, l = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < cut.w; ++p) {
+        const float2 ml = a.ml_part[partial(p) + r];
+        const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+        l += ml.y * w;
+        const float4 *part = reinterpret_cast<const float4 *>(a.o_part + partial(p) * D) + warp * Q * kRows + r;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+            const float4 v = part[i * kRows];
+            o[4 * i] += v.x * w;
+            o[4 * i + 1] += v.y * w;
+            o[4 * i + 2] += v.z * w;
+            o[4 * i + 3] += v.w * w;
         }
     }
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                         (static_cast<int64_t>(cut.x + k / a.group) * a.num_q_heads + cut.z * a.group + k % a.group) * D +
-                         lane * E;
+                         (static_cast<int64_t>(cut.x + r / a.group) * a.num_q_heads + cut.z * a.group + r % a.group) * D +
+                         warp * Q * 4;
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
+    for (int e = 0; e < 4 * Q; e += 2)
         *reinterpret_cast<__nv_bfloat162 *>(dst + e) = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
 }
 
-template <int D, int TILES>
-size_t tree_smem_bytes(int num_seqs) {
+template <int D>
+size_t tree_smem_bytes(int entries) {
     using Sh = TreeShape<D>;
-    const size_t bytes = TILES * Sh::kTileQ + 2 * tree_stages(TILES) * Sh::kTileKV + sizeof(TreeBars) +
-                         (static_cast<size_t>(num_seqs) + 1) * 8 + 1024;
-    // not more CTAs per SM than its 512 tensor-memory columns hold
-    return TILES == 1 ? (bytes < 80 * 1024 ? 80 * 1024 : bytes) : (bytes < 120 * 1024 ? 120 * 1024 : bytes);
+    const size_t bytes = Sh::kTileQ + 2 * kStages * Sh::kTileKV + sizeof(TreeBars) +
+                         (static_cast<size_t>(entries) + 1) * 4 + 1024;
+    return bytes < 80 * 1024 ? 80 * 1024 : bytes;  // not more than two CTAs per SM: tensor memory holds no more
 }
 
-template <int D, int BS, int TILES>
+template <int D, int BS>
 cudaError_t launch(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v, const TreeArgs &a,
                    int ctas, cudaStream_t stream) {
-    const size_t smem = tree_smem_bytes<D, TILES>(a.num_seqs);
-    auto *fn = paged_tree_kernel<D, BS, TILES>;
+    const size_t smem = tree_smem_bytes<D>(a.num_seqs * a.lists);
+    auto *fn = paged_tree_kernel<D, BS>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    fn<<<ctas, tree_threads(TILES), smem, stream>>>(tm_q, tm_k, tm_v, a);
+    fn<<<ctas, kThreads, smem, stream>>>(tm_q, tm_k, tm_v, a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.whole || ctas == 1) return e;
-    const int rows = (a.max_query_len < a.group_drafts ? a.max_query_len : a.group_drafts) * a.group;
+    const int rows = (a.max_query_len < a.tile_drafts ? a.max_query_len : a.tile_drafts) * a.group;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas - 1, (rows + kMergeWarps - 1) / kMergeWarps);
-    cfg.blockDim = dim3(kMergeWarps * 32);
+    cfg.gridDim = dim3(ctas - 1, (rows + kMergeRows - 1) / kMergeRows);
+    cfg.blockDim = dim3(kMergeRows * kMergeCols);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -707,21 +752,14 @@ cudaError_t launch(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUten
     return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a);
 }
 
-template <int TILES>
-cudaError_t launch_any(int D, int BS, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                       const TreeArgs &a, int ctas, cudaStream_t stream) {
-    if (D == 64) return BS == 16 ? launch<64, 16, TILES>(tm_q, tm_k, tm_v, a, ctas, stream)
-                                 : launch<64, 32, TILES>(tm_q, tm_k, tm_v, a, ctas, stream);
-    return BS == 16 ? launch<128, 16, TILES>(tm_q, tm_k, tm_v, a, ctas, stream)
-                    : launch<128, 32, TILES>(tm_q, tm_k, tm_v, a, ctas, stream);
-}
-
 }  // namespace
 
 cudaError_t tree_launch(int head_dim, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                         const TreeArgs &a, int ctas, cudaStream_t stream) {
-    return a.group_drafts > a.tile_drafts ? launch_any<2>(head_dim, a.block_size, tm_q, tm_k, tm_v, a, ctas, stream)
-                                          : launch_any<1>(head_dim, a.block_size, tm_q, tm_k, tm_v, a, ctas, stream);
+    if (head_dim == 64) return a.block_size == 16 ? launch<64, 16>(tm_q, tm_k, tm_v, a, ctas, stream)
+                                                  : launch<64, 32>(tm_q, tm_k, tm_v, a, ctas, stream);
+    return a.block_size == 16 ? launch<128, 16>(tm_q, tm_k, tm_v, a, ctas, stream)
+                              : launch<128, 32>(tm_q, tm_k, tm_v, a, ctas, stream);
 }
 
 }  // namespace pkv
