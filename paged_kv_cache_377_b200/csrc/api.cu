@@ -83,6 +83,26 @@ int make_pool_map(CUtensorMap *map, const void *pool, int num_blocks, int bs, in
     return PKV_OK;
 }
 
+// Tensor map over an e4m3 pool [num_blocks][bs][Hkv][D] seen as 3D (D, Hkv,
+// num_blocks*bs); one box = a block's rows of one kv head, swizzled over the
+// row's 128 or 64 bytes for the MMAs, or as they are.
+int make_code_map(CUtensorMap *map, const void *pool, int num_blocks, int bs, int hkv, int d, bool swizzle) {
+    auto fn = encode_fn();
+    if (!fn) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hkv),
+                          static_cast<cuuint64_t>(num_blocks) * bs};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hkv) * d};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(d), 1, static_cast<cuuint32_t>(bs)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(pool), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+    return PKV_OK;
+}
+
 // Tensor map over the queries q [T][Hkv][G][D] bf16 seen as 5D (64, D/64, G,
 // Hkv, T): one box = one 64-column slice of 128 / G query tokens x G heads,
 // i.e. 128 rows (token, head) of 128 bytes, 128-byte swizzled.
@@ -810,14 +830,14 @@ int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const voi
     a.num_blocks = num_blocks;
     a.scale_log2 = scale * 1.4426950408889634f;
     if (std::fabs(a.scale_log2) < 1e-30f) a.scale_log2 = 1e-30f;  // hidden logits are -inf: never times zero
-    if (fp8) {
-        const cudaError_t e = pkv::tree_simple_launch(true, head_dim, a, static_cast<cudaStream_t>(stream));
-        if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
-        return ok();
-    }
     CUtensorMap tm_q, tm_k, tm_v;
-    if ((rc = make_pool_map(&tm_k, k_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return rc;
-    if ((rc = make_pool_map(&tm_v, v_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    if (fp8) {
+        if ((rc = make_code_map(&tm_k, k_cache, num_blocks, block_size, num_kv_heads, head_dim, true)) != PKV_OK) return rc;
+        if ((rc = make_code_map(&tm_v, v_cache, num_blocks, block_size, num_kv_heads, head_dim, false)) != PKV_OK) return rc;
+    } else {
+        if ((rc = make_pool_map(&tm_k, k_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return rc;
+        if ((rc = make_pool_map(&tm_v, v_cache, num_blocks, block_size, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    }
     if ((rc = make_query_map(&tm_q, q, num_tokens, num_kv_heads, group, head_dim)) != PKV_OK) return rc;
     const TreeLayout lay = tree_layout(head_dim);
     char *ws = static_cast<char *>(workspace);
@@ -839,7 +859,8 @@ int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const voi
     if (per_seq > 0x7fffffff) return fail(PKV_ERR_UNSUPPORTED, "max_blocks_per_seq %d is too long for %lld heads and "
                                           "row tiles", max_blocks_per_seq, static_cast<long long>(num_kv_heads * tiles));
     const int64_t fit = 0x7fffffff / per_seq;
-    const int chunk = static_cast<int>(fit < pkv::kTreeMaxSeqs ? fit : pkv::kTreeMaxSeqs);
+    const int most = fp8 ? pkv::kTreeMaxSeqsFp8 : pkv::kTreeMaxSeqs;
+    const int chunk = static_cast<int>(fit < most ? fit : most);
     for (int s0 = 0; s0 < num_seqs; s0 += chunk) {
         a.num_seqs = num_seqs - s0 < chunk ? num_seqs - s0 : chunk;
         a.block_tables = block_tables + static_cast<int64_t>(s0) * max_blocks_per_seq;
@@ -850,7 +871,7 @@ int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const voi
         int64_t ctas = 2 * static_cast<int64_t>(sms);
         if (ctas > pkv::kTreeMaxCtas) ctas = pkv::kTreeMaxCtas;
         if (ctas > bound) ctas = bound;
-        const cudaError_t e = pkv::tree_launch(head_dim, tm_q, tm_k, tm_v, a, static_cast<int>(ctas),
+        const cudaError_t e = pkv::tree_launch(fp8, head_dim, tm_q, tm_k, tm_v, a, static_cast<int>(ctas),
                                                static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
     }

@@ -88,12 +88,13 @@ struct TreeArgs {
     unsigned *arrivals;           // [CTAs]: pieces stored of a two-piece segment, by first CTA; 0 between launches
 };
 
-constexpr int kTreeMaxSeqs = 1024;  // sequences of one launch (weights kept in shared memory)
+// Sequences of one launch: their weights share the memory of two CTAs per SM with the operands, and with the rings
+// of codes over e4m3 pools.
+constexpr int kTreeMaxSeqs = 1024, kTreeMaxSeqsFp8 = 512;
 constexpr int kTreeMaxCtas = 320;
 
-cudaError_t tree_launch(int head_dim, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                        const TreeArgs &args, int ctas, cudaStream_t stream);
-cudaError_t tree_simple_launch(bool fp8, int head_dim, const TreeArgs &args, cudaStream_t stream);
+cudaError_t tree_launch(bool fp8, int head_dim, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                        const CUtensorMap &tm_v, const TreeArgs &args, int ctas, cudaStream_t stream);
 
 // A step's bookkeeping on the GPU (tables.cu).
 cudaError_t tables_grow_launch(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_tokens,

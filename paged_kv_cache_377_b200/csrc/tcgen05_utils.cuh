@@ -15,9 +15,15 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
            (static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: bf16 x bf16 (or f16 x f16) -> fp32, A K-major, B K- or N-major.
-__host__ __device__ constexpr uint32_t instr_desc(int M, int N, bool b_n_major, bool f16 = false) {
-    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | ((b_n_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+// The same for 64-byte rows under the 64-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc_64b(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((lbo >> 4) & 0x3fffu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3fffu) << 32) | (1ull << 46) | (4ull << 61);
+}
+
+// Instruction descriptor: bf16 x bf16 (or format 0: f16, and e4m3 of kind::f8f6f4) -> fp32, A K-major, B K- or N-major.
+__host__ __device__ constexpr uint32_t instr_desc(int M, int N, bool b_n_major, bool format0 = false) {
+    return (1u << 4) | (format0 ? 0u : (1u << 7) | (1u << 10)) | ((b_n_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
@@ -25,6 +31,15 @@ __device__ __forceinline__ void umma(uint32_t tmem_d, uint64_t da, uint64_t db, 
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(tmem_d),
+        "l"(da), "l"(db), "r"(idesc), "r"(accumulate), "r"(0u)
+        : "memory");
+}
+
+// e4m3 operands, both K-major, 32 of them a step.
+__device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(tmem_d),
         "l"(da), "l"(db), "r"(idesc), "r"(accumulate), "r"(0u)
         : "memory");
 }

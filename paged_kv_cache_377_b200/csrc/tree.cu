@@ -24,7 +24,14 @@
 // fp32, and write P in bf16 beside S. The mask only matters in the iterations
 // that reach past the committed tokens: a row's bits for 64 positions are two
 // words there.
+// Over e4m3 pools S takes K's codes as they are: each row of Q, scaled by a power
+// of two, is split into two e4m3 terms (four bits each of its eight), and S = Q1 K^T
+// + Q2 K^T on kind::f8f6f4 costs what one bf16 product does. V is widened to f16 by
+// two warps, exactly, and P written in f16: e4m3 terms of P would lose the small
+// weights of a long context beside a large one. (Widening K to bf16 as well kept the
+// integer pipe busy for longer than the copies take.)
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "device_utils.cuh"
 #include "launch.h"
@@ -103,50 +110,176 @@ __device__ __forceinline__ uint2 visible_bits(const int32_t *row, int n, int fir
     return make_uint2(static_cast<uint32_t>(vis), static_cast<uint32_t>(vis >> 32));
 }
 
-template <int D>
+template <int D, bool FP8>
 struct TreeShape {
-    static constexpr int HALVES = D / 64;                     // 128-byte column slices of a row
+    static constexpr int HALVES = D / 64;                     // 128-byte column slices of a 16-bit row
     static constexpr uint32_t kHalfKV = kTokens * 128;
-    static constexpr uint32_t kTileKV = HALVES * kHalfKV;     // K (or V) of one stage
+    static constexpr uint32_t kTileV = HALVES * kHalfKV;      // V of one stage (16-bit)
+    static constexpr uint32_t kTileK = FP8 ? kTokens * D : kTileV;
     static constexpr uint32_t kQHalf = kRows * 128;
     static constexpr uint32_t kTileQ = HALVES * kQHalf;
+    // warps: 0 - 3 softmax; over bf16 pools the loaders of K and V and the MMAs; over e4m3 pools the loader of K, the
+    // MMAs and V's two (which widen)
+    static constexpr int kLoadK = 4, kLoadV = FP8 ? 6 : 5, kMma = FP8 ? 5 : 6, kThreads = FP8 ? 256 : 224;
+    // stages of the operand tiles and of the codes of V: what leaves room for two CTAs per SM
+    static constexpr int kStagesK = FP8 ? 3 : 2, kStagesV = 2, kRawV = 2;
+    static constexpr uint32_t kRawTile = kTokens * D;  // V's codes of one iteration
+    static constexpr uint32_t kRaw = FP8 ? kRawV * kRawTile : 0;
+    static constexpr uint32_t kOperands = kTileQ + kStagesK * kTileK + kStagesV * kTileV + kRaw;
 };
 
-constexpr int kStages = 2;
-constexpr int kSoftmaxWarps = 4, kLoadK = 4, kLoadV = 5, kMma = 6;
-constexpr int kThreads = 224;
+// Sixteen e4m3 codes as f16 times 2^-8: the exponent field keeps its bits, the bias differs by 8. Exact, subnormal
+// codes too; the two NaN codes come out as 480 (see has_nan). `k128` is 128: a multiply that the compiler cannot turn
+// into a shift, so that half of the work goes to the multipliers' pipe instead of the integer one.
+__device__ __forceinline__ void widen16(uint4 codes, uint4 &lo, uint4 &hi, uint32_t k128) {
+    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t h = __byte_perm(c[i / 2], 0, i & 1 ? 0x4342 : 0x4140);  // two codes, each in 16 bits
+        w[i] = (h & 0x00800080u) * k128 + h * k128;  // seven up, and the sign (added to itself) one more
+    }
+    lo = make_uint4(w[0], w[1], w[2], w[3]);
+    hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Bits of 0x80808080 set where a code is a NaN.
+__device__ __forceinline__ uint32_t has_nan(uint4 c) {
+    return ((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) |
+           ((c.z & 0x7f7f7f7fu) + 0x01010101u) | ((c.w & 0x7f7f7f7fu) + 0x01010101u);
+}
+
+__device__ __forceinline__ void mark_nans(uint4 codes, uint4 &lo, uint4 &hi) {
+    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t *w[2] = {&lo.x, &hi.x};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (((c[i / 4] >> (8 * (i % 4))) & 0x7fu) == 0x7fu)
+            w[i / 8][i / 2 % 4] |= 0x7e00u << (16 * (i & 1));
+}
+
+// A warp's `span` rows of codes (dense, D bytes each) into rows tok0 .. of an operand tile ([64-column half][row][128
+// bytes], swizzled). Eight rows of four 16-code chunks a step; rows and halves alternate so that neither side's banks
+// meet; four steps' codes are loaded before the first is stored (one by one, a step waited 280 cycles).
+template <int D>
+__device__ __forceinline__ void widen_rows(const uint8_t *src, uint8_t *dst, int tok0, int span, int lane) {
+    constexpr int HALVES = D / 64, BATCH = 4;
+    uint32_t k128;
+    asm volatile("mov.u32 %0, 128;" : "=r"(k128));
+    const int row = lane >> 2, chunk = lane & 3;
+    for (int i0 = 0; i0 < span / 8 * HALVES; i0 += BATCH) {
+        uint4 codes[BATCH];
+        uint32_t nan = 0;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = i0 + k, t = i / HALVES * 8 + row, hf = HALVES == 1 ? 0 : (i ^ row) & 1;
+            codes[k] = *reinterpret_cast<const uint4 *>(src + t * D + hf * 64 + chunk * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) nan |= has_nan(codes[k]);
+        const bool any = (nan & 0x80808080u) != 0;
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) {
+            const int i = i0 + k, t = i / HALVES * 8 + row, hf = HALVES == 1 ? 0 : (i ^ row) & 1;
+            uint4 lo, hi;
+            widen16(codes[k], lo, hi, k128);
+            if (any) mark_nans(codes[k], lo, hi);
+            uint8_t *at = dst + hf * (kTokens * 128) + (tok0 + t) * 128;
+            *reinterpret_cast<uint4 *>(at + (((2 * chunk) ^ (t & 7)) << 4)) = lo;
+            *reinterpret_cast<uint4 *>(at + (((2 * chunk + 1) ^ (t & 7)) << 4)) = hi;
+        }
+    }
+}
+
+// Row r of the query tile, in place: D bf16 become two rows of D e4m3 codes, q f = q1 + q2 with f a power of two that
+// puts the row's largest magnitude in [2^7, 2^8). q1 keeps four bits, q2 the next four (what is below 2^-10 of q f is
+// lost, 2^-17 of the row's largest). At D = 128 q1 takes the first 128-byte slab and q2 the second; at D = 64 they share
+// the slab's rows. Returns 1 / f (NaN for a row that is not finite: its logits all are).
+template <int D>
+__device__ __forceinline__ float split_query(uint8_t *sq, int r) {
+    constexpr int HALVES = D / 64;
+    uint8_t *row = sq + r * 128;
+    auto at = [&](int hf, int ch) { return reinterpret_cast<uint4 *>(row + hf * (kRows * 128) + ((ch ^ (r & 7)) << 4)); };
+    uint32_t q[HALVES * 32];
+#pragma unroll
+    for (int i = 0; i < HALVES * 8; ++i) {
+        const uint4 v = *at(i / 8, i % 8);
+        q[4 * i] = v.x;
+        q[4 * i + 1] = v.y;
+        q[4 * i + 2] = v.z;
+        q[4 * i + 3] = v.w;
+    }
+    uint32_t top = 0;  // largest magnitude: bf16 magnitudes order like their bits
+#pragma unroll
+    for (int i = 0; i < HALVES * 32; ++i) top = __vmaxu2(top, q[i] & 0x7fff7fffu);
+    const int e = static_cast<int>(max(top & 0xffffu, top >> 16) >> 7);  // exponent field
+    const float f = __uint_as_float(static_cast<uint32_t>(min(261 - e, 247)) << 23);  // 2^(134 - e), at most 2^120
+    uint32_t c1[HALVES * 16], c2[HALVES * 16];
+#pragma unroll
+    for (int i = 0; i < HALVES * 16; ++i) {
+        uint32_t w1 = 0, w2 = 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float2 v = bf16x2_to_float2(q[2 * i + k]);
+            v = make_float2(v.x * f, v.y * f);
+            const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
+            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+            const __nv_fp8x2_storage_t rest =
+                __nv_cvt_float2_to_fp8x2(make_float2(v.x - b.x, v.y - b.y), __NV_SATFINITE, __NV_E4M3);
+            w1 |= static_cast<uint32_t>(a) << (16 * k);
+            w2 |= static_cast<uint32_t>(rest) << (16 * k);
+        }
+        c1[i] = w1;
+        c2[i] = w2;
+    }
+#pragma unroll
+    for (int i = 0; i < HALVES * 4; ++i) {
+        const uint4 v1 = make_uint4(c1[4 * i], c1[4 * i + 1], c1[4 * i + 2], c1[4 * i + 3]);
+        const uint4 v2 = make_uint4(c2[4 * i], c2[4 * i + 1], c2[4 * i + 2], c2[4 * i + 3]);
+        *at(0, i) = v1;
+        *(HALVES == 2 ? at(HALVES - 1, i) : at(0, 4 + i)) = v2;
+    }
+    return e == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(max(e - 7, 7)) << 23);
+}
+
+constexpr int kSoftmaxWarps = 4;
 constexpr uint32_t kTmemCols = 256;  // S | two buffers of P | O: two CTAs fill an SM's 512
 
 struct TreeBars {
-    uint64_t q_full, q_empty, done;
-    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t q_full, q_ready, q_empty, done;  // (q_ready: e4m3, the queries are split)
+    uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+    uint64_t raw_full[2][2];  // e4m3: V's codes, first and second 32 tokens
     // S is in tensor memory; the softmax threads have loaded it; P (buffer b) is written; O += P V of buffer b is
     // done; the piece's O is done
     uint64_t s_full, s_free, p_ready[2], pv_free[2], o_full;
     uint64_t all;  // the softmax warps meet
     int scan[16];
-    uint32_t bad[kBadRing];
+    uint32_t bad[kBadRing];  // blocks without a place in the pool, a bit each
     uint32_t tmem;
     int abort;
     int arrived;
     int poison[2];
 };
 
-template <int D, int BS>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D, int BS, bool FP8>
+__global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
     paged_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
-    using Sh = TreeShape<D>;
-    constexpr int HALVES = Sh::HALVES, BPI = kTokens / BS;
+    using Sh = TreeShape<D, FP8>;
+    constexpr int HALVES = Sh::HALVES, BPI = kTokens / BS, kThreads = Sh::kThreads;
+    constexpr int kStagesK = Sh::kStagesK, kStagesV = Sh::kStagesV;
+    constexpr int kLoadK = Sh::kLoadK, kLoadV = Sh::kLoadV, kMma = Sh::kMma;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // ---- shared memory: Q | K stages | V stages | barriers | weights before each entry
+    // ---- shared memory: Q | K stages | V stages | V's codes | barriers | weights before each entry
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sq = base;
     uint8_t *sk = sq + Sh::kTileQ;
-    uint8_t *sv = sk + kStages * Sh::kTileKV;
-    TreeBars &B = *reinterpret_cast<TreeBars *>(sv + kStages * Sh::kTileKV);
+    uint8_t *sv = sk + kStagesK * Sh::kTileK;
+    uint8_t *raw = sv + kStagesV * Sh::kTileV;
+    TreeBars &B = *reinterpret_cast<TreeBars *>(raw + Sh::kRaw);
     int *wp = reinterpret_cast<int *>(&B + 1);
 
     // ---- weights: every CTA sums over all sequences (one contiguous run per thread)
@@ -237,11 +370,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_init(&B.s_free, kSoftmaxWarps);
         mbar_init(&B.o_full, 1);
         mbar_init(&B.all, kSoftmaxWarps);
-        for (int i = 0; i < kStages; ++i) {
+        mbar_init(&B.q_ready, kSoftmaxWarps);
+        for (int i = 0; i < kStagesK; ++i) {
             mbar_init(&B.k_full[i], 1);
             mbar_init(&B.k_empty[i], 1);
-            mbar_init(&B.v_full[i], 1);
+        }
+        for (int i = 0; i < kStagesV; ++i) {
+            mbar_init(&B.v_full[i], FP8 ? 2 : 1);
             mbar_init(&B.v_empty[i], 1);
+            mbar_init(&B.raw_full[0][i], 1);
+            mbar_init(&B.raw_full[1][i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&B.p_ready[i], kSoftmaxWarps);
@@ -259,20 +397,38 @@ __global__ void __launch_bounds__(kThreads, 2)
     volatile int *abort_flag = &B.abort;
     const uint32_t tbase = B.tmem;
 
-    if (warp == kLoadK || warp == kLoadV) {
-        // ---------------- load warps: lane j copies one 128-byte column slice of one block
+    uint32_t q_loads = 0;
+    // The piece's queries, once the MMAs of the piece before are done with theirs (K's first loader).
+    auto load_q = [&](const Walk &w) {
+        if (q_loads > 0 && !warp_wait(&B.q_empty, (q_loads - 1) & 1u, abort_flag, a.status)) return false;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&B.q_full, HALVES * a.tile_drafts * a.group * 128);
+#pragma unroll
+            for (int q = 0; q < HALVES; ++q)
+                tma_load_5d(sq + q * Sh::kQHalf, &tm_q, &B.q_full, 0, q, 0, w.h, w.q0 + w.i0);
+        }
+        __syncwarp();
+        ++q_loads;
+        return true;
+    };
+
+    if (warp == kLoadK || (!FP8 && warp == kLoadV)) {
+        // ---------------- load warps: lane j copies one block, or one 128-byte column slice of it (16-bit rows)
+        constexpr int kStages = FP8 ? kStagesK : kStagesV, kSlices = FP8 ? 1 : HALVES;
+        constexpr uint32_t kTile = Sh::kTileK, kRowBytes = FP8 ? D : 128;
+        static_assert(FP8 || kStagesK == kStagesV, "K and V alike");
         const bool is_v = warp == kLoadV;
         uint8_t *ring = is_v ? sv : sk;
         uint64_t *full = is_v ? B.v_full : B.k_full, *empty = is_v ? B.v_empty : B.k_empty;
-        const int jb = lane / HALVES, hf = lane % HALVES;
+        const int jb = lane % BPI, hf = lane / BPI;
+        const bool has = lane < BPI * kSlices;
         auto entry = [&](const Walk &w) {  // this lane's table entry of the iteration, -1: no such block
             const int b = w.it * BPI + jb;
-            return lane < BPI * HALVES && b * BS < w.L
-                       ? __ldg(a.block_tables + static_cast<int64_t>(w.s) * a.max_blocks_per_seq + b)
-                       : -1;
+            return has && b * BS < w.L ? __ldg(a.block_tables + static_cast<int64_t>(w.s) * a.max_blocks_per_seq + b)
+                                       : -1;
         };
-        uint32_t g = 0, pieces = 0;
-        bool more = walk.next_piece(a, wp), ok = true, fresh = true, q_issued = false;
+        uint32_t g = 0;
+        bool more = walk.next_piece(a, wp), ok = true, fresh = true;
         int p = more ? entry(walk) : -1;
         while (more) {
             Walk ahead = walk;
@@ -280,33 +436,25 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int p2 = more2 ? entry(ahead) : -1;  // in flight while this iteration waits
             const int st = g % kStages;
             if (g >= kStages && !(ok = warp_wait(&empty[st], (g / kStages - 1) & 1u, abort_flag, a.status))) break;
-            const bool there = lane < BPI * HALVES && (walk.it * BPI + jb) * BS < walk.L;
+            const bool there = has && (walk.it * BPI + jb) * BS < walk.L;
             const bool mine = there && p >= 0 && p < a.num_blocks;
             const unsigned m = __ballot_sync(0xffffffffu, mine), lost = __ballot_sync(0xffffffffu, there && !mine);
             if (!is_v) {
                 if (lost && lane == 0) atomicOr(a.status, PKV_STATUS_BAD_BLOCK_ID);
-                if (lane == 0) B.bad[g % kBadRing] = lost;
+                if (lane == 0) B.bad[g % kBadRing] = lost & ((1u << BPI) - 1u);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(m)) * BS * 128u);
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(m)) * BS * kRowBytes);
             __syncwarp();
-            if (mine)
-                tma_load_4d(ring + st * Sh::kTileKV + hf * Sh::kHalfKV + jb * BS * 128, is_v ? &tm_v : &tm_k,
-                            &full[st], 0, hf, walk.h, p * BS);
+            if (mine) {
+                if (FP8)
+                    tma_load_3d(ring + st * kTile + jb * BS * D, &tm_k, &full[st], 0, walk.h, p * BS);
+                else
+                    tma_load_4d(ring + st * kTile + hf * Sh::kHalfKV + jb * BS * 128, is_v ? &tm_v : &tm_k, &full[st], 0,
+                                hf, walk.h, p * BS);
+            }
             ++g;
-            if (!is_v && fresh) {
-                // the piece's queries, once the MMAs of the piece before are done with theirs
-                if (pieces > 0 && !(ok = warp_wait(&B.q_empty, (pieces - 1) & 1u, abort_flag, a.status))) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&B.q_full, HALVES * a.tile_drafts * a.group * 128);
-#pragma unroll
-                    for (int q = 0; q < HALVES; ++q)
-                        tma_load_5d(sq + q * Sh::kQHalf, &tm_q, &B.q_full, 0, q, 0, walk.h, walk.q0 + walk.i0);
-                }
-                __syncwarp();
-                q_issued = true;
-                ++pieces;
-            }
+            if (!is_v && fresh && !(ok = load_q(walk))) break;
             fresh = more2 && ahead.it == ahead.it0;
             walk = ahead;
             more = more2;
@@ -314,38 +462,95 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         // copies still in flight (only after a wait gave up) land before exit
         if (!ok || *abort_flag) {
-            if (q_issued) mbar_wait_drain(&B.q_full, (pieces - 1) & 1u, a.status);
+            if (q_loads > 0) mbar_wait_drain(&B.q_full, (q_loads - 1) & 1u, a.status);
             for (uint32_t u = g > kStages ? g - kStages : 0; u < g; ++u)
                 mbar_wait_drain(&full[u % kStages], (u / kStages) & 1u, a.status);
         }
+        __syncwarp();
+    } else if (FP8 && warp >= kLoadV) {
+        // ---------------- V's warps over e4m3 pools, 32 tokens each: codes into the warp's own ring, widened into the
+        // operand tile, and the ring's stage filled again.
+        constexpr int kSpan = kTokens / 2, kBlocks = kSpan / BS, kRings = Sh::kRawV;
+        const int part = warp - kLoadV, tok0 = part * kSpan;
+        uint8_t *ring = raw + part * kRings * kSpan * D;
+        uint64_t *filled = B.raw_full[part];
+        const bool has = lane < kBlocks;
+        auto entry = [&](const Walk &w) {
+            const int b = w.it * BPI + part * kBlocks + lane;
+            return has && b * BS < w.L ? __ldg(a.block_tables + static_cast<int64_t>(w.s) * a.max_blocks_per_seq + b)
+                                       : -1;
+        };
+        uint32_t issued = 0, g = 0;
+        bool more = walk.next_piece(a, wp), ok = true;
+        int p = more ? entry(walk) : -1;
+        auto issue = [&]() {  // the next iteration's codes into its ring stage
+            Walk ahead = walk;
+            const bool more2 = ahead.next(a, wp);
+            const int p2 = more2 ? entry(ahead) : -1, st = issued % kRings;
+            const bool mine = p >= 0 && p < a.num_blocks;
+            const unsigned m = __ballot_sync(0xffffffffu, mine);
+            if (lane == 0) mbar_arrive_expect_tx(&filled[st], static_cast<uint32_t>(__popc(m)) * BS * D);
+            __syncwarp();
+            if (mine)
+                tma_load_3d(ring + (st * kSpan + lane * BS) * D, &tm_v, &filled[st], 0, walk.h, p * BS);
+            ++issued;
+            walk = ahead;
+            more = more2;
+            p = p2;
+        };
+        while (more && issued < kRings) issue();
+        while (g < issued) {
+            const int st = g % kRings, sv_st = g % kStagesV;
+            if (!(ok = warp_wait(&filled[st], (g / kRings) & 1u, abort_flag, a.status))) break;
+            if (g >= kStagesV && !(ok = warp_wait(&B.v_empty[sv_st], (g / kStagesV - 1) & 1u, abort_flag, a.status))) break;
+            widen_rows<D>(ring + st * kSpan * D, sv + sv_st * Sh::kTileV, tok0, kSpan, lane);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.v_full[sv_st]);
+            ++g;
+            if (more) issue();
+        }
+        if (!ok || *abort_flag)
+            for (uint32_t u = g; u < issued; ++u) mbar_wait_drain(&filled[u % kRings], (u / kRings) & 1u, a.status);
         __syncwarp();
     } else if (warp == kMma) {
         // ---------------- MMA warp: one elected lane issues. S(it + 1) is issued as soon as the softmax warps hold
         // S(it) in registers, and runs while they work on it; O += P(it) V(it) follows P(it).
         const bool leader = elect_one();
-        const uint64_t dq = smem_desc(smem_u32(sq), 16, 1024), dk = smem_desc(smem_u32(sk), 16, 1024),
+        const uint64_t dq = smem_desc(smem_u32(sq), 16, 1024),
+                       dk = FP8 && D == 64 ? smem_desc_64b(smem_u32(sk), 16, 512) : smem_desc(smem_u32(sk), 16, 1024),
                        dv = smem_desc(smem_u32(sv), Sh::kHalfKV, 1024);
         const uint32_t t_p = tbase + 64, t_o = tbase + 128;
         Walk ws = walk, wv = walk;
         uint32_t gs = 0, gv = 0, pieces = 0;
         bool ok = true;
         auto step_s = [&]() {
-            const int st = gs % kStages;
+            const int st = gs % kStagesK;
             if (ws.it == ws.it0) {
-                if (!(ok = warp_wait(&B.q_full, pieces & 1u, abort_flag, a.status))) return;
+                if (!(ok = warp_wait(FP8 ? &B.q_ready : &B.q_full, pieces & 1u, abort_flag, a.status))) return;
                 ++pieces;
             }
-            if (!(ok = warp_wait(&B.k_full[st], (gs / kStages) & 1u, abort_flag, a.status))) return;
+            if (!(ok = warp_wait(&B.k_full[st], (gs / kStagesK) & 1u, abort_flag, a.status))) return;
             if (gs > 0 && !(ok = warp_wait(&B.s_free, (gs - 1) & 1u, abort_flag, a.status))) return;
             tc_fence_after();
             if (leader) {
+                if (FP8) {  // the two terms of Q against the same codes, 32 of them a step
 #pragma unroll
-                for (int hf = 0; hf < HALVES; ++hf)
+                    for (int term = 0; term < 2; ++term)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma(tbase, dq + ((hf * Sh::kQHalf + kk * 32) >> 4),
-                             dk + ((st * Sh::kTileKV + hf * Sh::kHalfKV + kk * 32) >> 4),
-                             instr_desc(128, kTokens, false), (hf | kk) != 0);
+                        for (int kk = 0; kk < D / 32; ++kk)
+                            umma_f8(tbase, dq + ((term * (HALVES == 2 ? Sh::kQHalf : 64) + kk * 32) >> 4),
+                                    dk + ((st * Sh::kTileK + kk * 32) >> 4), instr_desc(128, kTokens, false, true),
+                                    (term | kk) != 0);
+                } else {
+#pragma unroll
+                    for (int hf = 0; hf < HALVES; ++hf)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma(tbase, dq + ((hf * Sh::kQHalf + kk * 32) >> 4),
+                                 dk + ((st * Sh::kTileK + hf * Sh::kHalfKV + kk * 32) >> 4),
+                                 instr_desc(128, kTokens, false), (hf | kk) != 0);
+                }
                 umma_commit(&B.s_full);
                 umma_commit(&B.k_empty[st]);
                 if (ws.it + 1 == ws.it1) umma_commit(&B.q_empty);
@@ -354,16 +559,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             ++gs;
         };
         auto step_v = [&]() {
-            const int st = gv % kStages;
+            const int st = gv % kStagesV;
             const uint32_t b = gv & 1u;
-            if (!(ok = warp_wait(&B.v_full[st], (gv / kStages) & 1u, abort_flag, a.status))) return;
+            if (!(ok = warp_wait(&B.v_full[st], (gv / kStagesV) & 1u, abort_flag, a.status))) return;
             if (!(ok = warp_wait(&B.p_ready[b], (gv >> 1) & 1u, abort_flag, a.status))) return;
             tc_fence_after();
             if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_ts(t_o, t_p + 32 * b + kk * 8, dv + ((st * Sh::kTileKV + kk * 16 * 128) >> 4),
-                            instr_desc(128, D, true), wv.it != wv.it0 || kk != 0);
+                    umma_ts(t_o, t_p + 32 * b + kk * 8, dv + ((st * Sh::kTileV + kk * 16 * 128) >> 4),
+                            instr_desc(128, D, true, FP8), wv.it != wv.it0 || kk != 0);
                 umma_commit(&B.pv_free[b]);
                 umma_commit(&B.v_empty[st]);
                 if (wv.it + 1 == wv.it1) umma_commit(&B.o_full);
@@ -377,7 +582,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             more_s = ok && ws.next(a, wp);
         }
         while (ok && more_v) {
-            if (more_s) {
+            // (over e4m3 pools the softmax warps split a piece's queries when they are through with the piece before:
+            // its last P V cannot wait for the next piece's first S)
+            const bool late = FP8 && more_s && ws.it == ws.it0;
+            if (more_s && !late) {
                 step_s();
                 if (!ok) break;
                 more_s = ws.next(a, wp);
@@ -385,6 +593,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             step_v();
             if (!ok) break;
             more_v = wv.next(a, wp);
+            if (late) {
+                step_s();
+                more_s = ok && ws.next(a, wp);
+            }
         }
         // every MMA issued is done before the tensor memory is freed (one phase: nothing aliases)
         if (leader) umma_commit(&B.done);
@@ -396,8 +608,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int r = tid;
         const uint32_t t_s = tbase + (static_cast<uint32_t>(warp * 32) << 16), t_p = t_s + 64, t_o = t_s + 128;
         const int G = a.group;
-        const float c2 = fabsf(a.scale_log2);
-        const bool negative = a.scale_log2 < 0.f, spare = r >= a.tile_drafts * G;
+        float c2 = fabsf(a.scale_log2), v_scale = 1.f;
+        bool negative = a.scale_log2 < 0.f;
+        const bool spare = r >= a.tile_drafts * G;
         volatile int *poison = B.poison;
         uint32_t g = 0, pieces = 0, met_all = 0;
         bool ok = true;
@@ -414,6 +627,17 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int draft = walk.i0 + r / G;
             const bool live = !spare && draft < walk.n;
             const bool warp_live = __any_sync(0xffffffffu, live);
+            if (FP8) {
+                // Queries are split by the threads that own them. The head's K scale and the split's factor go into
+                // the logits' factor, V's scale (and the f16 codes' 2^8) into O.
+                if (!(ok = warp_wait(&B.q_full, piece & 1u, abort_flag, a.status))) break;
+                const float f = a.scale_log2 * __ldg(a.k_scale + walk.h) * (warp_live ? split_query<D>(sq, r) : 1.f);
+                fence_proxy_async_shared();
+                signal(&B.q_ready);
+                c2 = fabsf(f) < 1e-37f ? 1e-37f : fabsf(f);
+                negative = f < 0.f;
+                v_scale = __ldg(a.v_scale + walk.h) * 256.f;
+            }
             const int first = walk.L - walk.n;  // first draft's position
             const int32_t *bits = a.tree_mask + static_cast<int64_t>(walk.q0 + min(draft, walk.n - 1)) * a.mask_words;
             float m_ref = -INFINITY, l_run = 0.f;
@@ -440,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (bad) {
 #pragma unroll
                             for (int k = 0; k < BPI; ++k) {
-                                if (!((bad >> (k * HALVES)) & 1u)) continue;
+                                if (!((bad >> k) & 1u)) continue;
                                 const uint32_t gone = BS == 32 ? ~0u : 0xffffu << (k % 2 * 16);
                                 if (k * BS < 32)
                                     vis.x &= ~gone;
@@ -487,8 +711,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 ps2b = fadd2(ps2b, pr);
                             else
                                 ps2a = fadd2(ps2a, pr);
-                            const __nv_bfloat162 v2 = __floats2bfloat162_rn(pr.x, pr.y);
-                            w[e] = *reinterpret_cast<const uint32_t *>(&v2);
+                            if (FP8) {
+                                const __half2 v2 = __floats2half2_rn(pr.x, pr.y);
+                                w[e] = *reinterpret_cast<const uint32_t *>(&v2);
+                            } else {
+                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(pr.x, pr.y);
+                                w[e] = *reinterpret_cast<const uint32_t *>(&v2);
+                            }
                         }
                         tmem_st16(t_p + 32 * b + 16 * part, w);
                     }
@@ -513,13 +742,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                 // P = 0 there multiplies zeros. A draft's V that is not finite is hidden from the rows that do not
                 // see it in the same way, and added back to the others at the end.
                 if (tail || bad) {
-                    const int st = g % kStages;
-                    if (!(ok = warp_wait(&B.v_full[st], (g / kStages) & 1u, abort_flag, a.status))) break;
-                    uint8_t *vt = sv + st * Sh::kTileKV;
+                    const int st = g % kStagesV;
+                    if (!(ok = warp_wait(&B.v_full[st], (g / kStagesV) & 1u, abort_flag, a.status))) break;
+                    uint8_t *vt = sv + st * Sh::kTileV;
+                    constexpr uint32_t kOdd = FP8 ? 0x7c00u : 0x7f80u;  // exponent of an infinity or a NaN
                     for (int e = r; e < HALVES * kTokens * 8; e += 128) {
                         const int hf = e / (kTokens * 8), tok = (e / 8) % kTokens, ch = e % 8;
                         uint4 *at = reinterpret_cast<uint4 *>(vt + hf * Sh::kHalfKV + tok * 128 + ((ch ^ (tok & 7)) << 4));
-                        if (t0 + tok >= walk.L || ((bad >> (tok / BS * HALVES)) & 1u)) {
+                        if (t0 + tok >= walk.L || ((bad >> (tok / BS)) & 1u)) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
                         } else if (t0 + tok >= first) {
                             uint4 v = *at;
@@ -527,11 +757,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                             bool any = false;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                if ((w[i] & 0x7f80u) == 0x7f80u) {
+                                if ((w[i] & kOdd) == kOdd) {
                                     w[i] &= 0xffff0000u;
                                     any = true;
                                 }
-                                if ((w[i] & 0x7f800000u) == 0x7f800000u) {
+                                if ((w[i] & (kOdd << 16)) == kOdd << 16) {
                                     w[i] &= 0x0000ffffu;
                                     any = true;
                                 }
@@ -606,17 +836,27 @@ __global__ void __launch_bounds__(kThreads, 2)
                                 const int p =
                                     __ldg(a.block_tables + static_cast<int64_t>(walk.s) * a.max_blocks_per_seq + pos / BS);
                                 if (p < 0 || p >= a.num_blocks) continue;
-                                const __nv_bfloat16 *v =
-                                    static_cast<const __nv_bfloat16 *>(a.v_cache) +
-                                    ((static_cast<int64_t>(p) * BS + pos % BS) * a.num_kv_heads + walk.h) * D + col;
+                                const int64_t at = ((static_cast<int64_t>(p) * BS + pos % BS) * a.num_kv_heads + walk.h) * D + col;
+                                if (FP8) {
+                                    const uint8_t *v = static_cast<const uint8_t *>(a.v_cache) + at;
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) {
-                                    const float f = __bfloat162float(v[i]);
-                                    if (!isfinite(f)) o[i] += f;
+                                    for (int i = 0; i < 32; ++i)
+                                        if ((v[i] & 0x7fu) == 0x7fu) o[i] = NAN;
+                                } else {
+                                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_cache) + at;
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) {
+                                        const float f = __bfloat162float(v[i]);
+                                        if (!isfinite(f)) o[i] += f;
+                                    }
                                 }
                             }
                         }
                         if (!live) continue;
+                        if (FP8) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= v_scale;
+                        }
                         // a partial is [columns / 4][rows][4]: a warp's rows are side by side
                         if (store) {
                             float4 *part = reinterpret_cast<float4 *>(a.o_part + own_row * D) + (col / 4) * kRows + r;
@@ -722,22 +962,20 @@ __global__ void __launch_bounds__(kMergeRows * kMergeCols) tree_merge_kernel(con
         *reinterpret_cast<__nv_bfloat162 *>(dst + e) = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
 }
 
-template <int D>
+template <int D, bool FP8>
 size_t tree_smem_bytes(int entries) {
-    using Sh = TreeShape<D>;
-    const size_t bytes = Sh::kTileQ + 2 * kStages * Sh::kTileKV + sizeof(TreeBars) +
-                         (static_cast<size_t>(entries) + 1) * 4 + 1024;
+    const size_t bytes = TreeShape<D, FP8>::kOperands + sizeof(TreeBars) + (static_cast<size_t>(entries) + 1) * 4 + 1024;
     return bytes < 80 * 1024 ? 80 * 1024 : bytes;  // not more than two CTAs per SM: tensor memory holds no more
 }
 
-template <int D, int BS>
+template <int D, int BS, bool FP8>
 cudaError_t launch(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v, const TreeArgs &a,
                    int ctas, cudaStream_t stream) {
-    const size_t smem = tree_smem_bytes<D>(a.num_seqs * a.lists);
-    auto *fn = paged_tree_kernel<D, BS>;
+    const size_t smem = tree_smem_bytes<D, FP8>(a.num_seqs * a.lists);
+    auto *fn = paged_tree_kernel<D, BS, FP8>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    fn<<<ctas, kThreads, smem, stream>>>(tm_q, tm_k, tm_v, a);
+    fn<<<ctas, TreeShape<D, FP8>::kThreads, smem, stream>>>(tm_q, tm_k, tm_v, a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.whole || ctas == 1) return e;
     const int rows = (a.max_query_len < a.tile_drafts ? a.max_query_len : a.tile_drafts) * a.group;
     cudaLaunchConfig_t cfg{};
@@ -752,14 +990,21 @@ cudaError_t launch(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUten
     return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a);
 }
 
+template <bool FP8>
+cudaError_t launch_any(int D, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                       const TreeArgs &a, int ctas, cudaStream_t stream) {
+    if (D == 64) return a.block_size == 16 ? launch<64, 16, FP8>(tm_q, tm_k, tm_v, a, ctas, stream)
+                                           : launch<64, 32, FP8>(tm_q, tm_k, tm_v, a, ctas, stream);
+    return a.block_size == 16 ? launch<128, 16, FP8>(tm_q, tm_k, tm_v, a, ctas, stream)
+                              : launch<128, 32, FP8>(tm_q, tm_k, tm_v, a, ctas, stream);
+}
+
 }  // namespace
 
-cudaError_t tree_launch(int head_dim, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                        const TreeArgs &a, int ctas, cudaStream_t stream) {
-    if (head_dim == 64) return a.block_size == 16 ? launch<64, 16>(tm_q, tm_k, tm_v, a, ctas, stream)
-                                                  : launch<64, 32>(tm_q, tm_k, tm_v, a, ctas, stream);
-    return a.block_size == 16 ? launch<128, 16>(tm_q, tm_k, tm_v, a, ctas, stream)
-                              : launch<128, 32>(tm_q, tm_k, tm_v, a, ctas, stream);
+cudaError_t tree_launch(bool fp8, int head_dim, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                        const CUtensorMap &tm_v, const TreeArgs &a, int ctas, cudaStream_t stream) {
+    return fp8 ? launch_any<true>(head_dim, tm_q, tm_k, tm_v, a, ctas, stream)
+               : launch_any<false>(head_dim, tm_q, tm_k, tm_v, a, ctas, stream);
 }
 
 }  // namespace pkv

@@ -92,6 +92,17 @@ def test_many_sequences(fp8):
           "2500 sequences")
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_e4m3_code(D):
+    """Zeros, subnormal codes and the largest ones, of both signs, in K and in V."""
+    step = make_step(27, [256, 70], [30, 5], 8, 2, D, 16, fp8=True, scale=0.004)
+    rng = np.random.default_rng(27)
+    for pool in (step.k_cache, step.v_cache):
+        codes = torch.from_numpy(rng.integers(0, 127, size=tuple(pool.shape)) | (rng.integers(0, 2, size=tuple(pool.shape)) << 7))
+        pool[:] = torch.where(pool == 0x7F, pool, codes.to(torch.uint8))
+    check(step, "all codes")
+
+
 def poison(step, s, drafts, nan_k, value):
     bs = step.k_cache.shape[1]
     base = int(step.context_lens[s]) - len(step.sees[s])
