@@ -128,65 +128,35 @@ struct TreeShape {
     static constexpr uint32_t kOperands = kTileQ + kStagesK * kTileK + kStagesV * kTileV + kRaw;
 };
 
-// Sixteen e4m3 codes as f16 times 2^-8: the exponent field keeps its bits, the bias differs by 8. Exact, subnormal
-// codes too; the two NaN codes come out as 480 (see has_nan). `k128` is 128: a multiply that the compiler cannot turn
-// into a shift, so that half of the work goes to the multipliers' pipe instead of the integer one.
-__device__ __forceinline__ void widen16(uint4 codes, uint4 &lo, uint4 &hi, uint32_t k128) {
-    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t h = __byte_perm(c[i / 2], 0, i & 1 ? 0x4342 : 0x4140);  // two codes, each in 16 bits
-        w[i] = (h & 0x00800080u) * k128 + h * k128;  // seven up, and the sign (added to itself) one more
-    }
-    lo = make_uint4(w[0], w[1], w[2], w[3]);
-    hi = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
-// Bits of 0x80808080 set where a code is a NaN.
-__device__ __forceinline__ uint32_t has_nan(uint4 c) {
-    return ((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) |
-           ((c.z & 0x7f7f7f7fu) + 0x01010101u) | ((c.w & 0x7f7f7f7fu) + 0x01010101u);
-}
-
-__device__ __forceinline__ void mark_nans(uint4 codes, uint4 &lo, uint4 &hi) {
-    const uint32_t c[4] = {codes.x, codes.y, codes.z, codes.w};
-    uint32_t *w[2] = {&lo.x, &hi.x};
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        if (((c[i / 4] >> (8 * (i % 4))) & 0x7fu) == 0x7fu)
-            w[i / 8][i / 2 % 4] |= 0x7e00u << (16 * (i & 1));
-}
-
 // A warp's `span` rows of codes (dense, D bytes each) into rows tok0 .. of an operand tile ([64-column half][row][128
-// bytes], swizzled). Eight rows of four 16-code chunks a step; rows and halves alternate so that neither side's banks
-// meet; four steps' codes are loaded before the first is stored (one by one, a step waited 280 cycles).
+// bytes], swizzled), as f16 (exact). Eight rows of four 16-code chunks a step; rows and halves alternate so that neither
+// side's banks meet; four steps' codes are loaded before the first is stored (one by one, a step waited 280 cycles).
+// The hardware's conversion takes two codes in 2 cycles a warp; placing their bits by hand took 8.
 template <int D>
 __device__ __forceinline__ void widen_rows(const uint8_t *src, uint8_t *dst, int tok0, int span, int lane) {
     constexpr int HALVES = D / 64, BATCH = 4;
-    uint32_t k128;
-    asm volatile("mov.u32 %0, 128;" : "=r"(k128));
     const int row = lane >> 2, chunk = lane & 3;
     for (int i0 = 0; i0 < span / 8 * HALVES; i0 += BATCH) {
         uint4 codes[BATCH];
-        uint32_t nan = 0;
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const int i = i0 + k, t = i / HALVES * 8 + row, hf = HALVES == 1 ? 0 : (i ^ row) & 1;
             codes[k] = *reinterpret_cast<const uint4 *>(src + t * D + hf * 64 + chunk * 16);
         }
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) nan |= has_nan(codes[k]);
-        const bool any = (nan & 0x80808080u) != 0;
-#pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const int i = i0 + k, t = i / HALVES * 8 + row, hf = HALVES == 1 ? 0 : (i ^ row) & 1;
-            uint4 lo, hi;
-            widen16(codes[k], lo, hi, k128);
-            if (any) mark_nans(codes[k], lo, hi);
+            const uint32_t c[4] = {codes[k].x, codes[k].y, codes[k].z, codes[k].w};
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                    static_cast<__nv_fp8x2_storage_t>(e & 1 ? c[e / 2] >> 16 : c[e / 2] & 0xffffu), __NV_E4M3);
+                w[e] = *reinterpret_cast<const uint32_t *>(&h);
+            }
             uint8_t *at = dst + hf * (kTokens * 128) + (tok0 + t) * 128;
-            *reinterpret_cast<uint4 *>(at + (((2 * chunk) ^ (t & 7)) << 4)) = lo;
-            *reinterpret_cast<uint4 *>(at + (((2 * chunk + 1) ^ (t & 7)) << 4)) = hi;
+            *reinterpret_cast<uint4 *>(at + (((2 * chunk) ^ (t & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(at + (((2 * chunk + 1) ^ (t & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
         }
     }
 }
@@ -629,14 +599,14 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             const bool warp_live = __any_sync(0xffffffffu, live);
             if (FP8) {
                 // Queries are split by the threads that own them. The head's K scale and the split's factor go into
-                // the logits' factor, V's scale (and the f16 codes' 2^8) into O.
+                // the logits' factor, V's scale into O.
                 if (!(ok = warp_wait(&B.q_full, piece & 1u, abort_flag, a.status))) break;
                 const float f = a.scale_log2 * __ldg(a.k_scale + walk.h) * (warp_live ? split_query<D>(sq, r) : 1.f);
                 fence_proxy_async_shared();
                 signal(&B.q_ready);
                 c2 = fabsf(f) < 1e-37f ? 1e-37f : fabsf(f);
                 negative = f < 0.f;
-                v_scale = __ldg(a.v_scale + walk.h) * 256.f;
+                v_scale = __ldg(a.v_scale + walk.h);
             }
             const int first = walk.L - walk.n;  // first draft's position
             const int32_t *bits = a.tree_mask + static_cast<int64_t>(walk.q0 + min(draft, walk.n - 1)) * a.mask_words;
