@@ -85,7 +85,8 @@ struct TreeArgs {
     float *o_part;                // fp32 [2 * CTAs][D / 4][128][4]: a CTA's partials of a continued and of a begun segment
     float2 *ml_part;              // their rows' maximum (log2 domain) and sum
     int4 *cuts;                   // [CTAs]: the segment of over two pieces that a CTA begins (see tree_merge_kernel)
-    unsigned *arrivals;           // [CTAs]: pieces stored of a two-piece segment, by first CTA; 0 between launches
+    unsigned *arrivals;           // [CTAs], by a two-piece segment's first CTA: pieces that have ended + 16 x warps that
+                                  // have stored the first one's partial; 0 between launches
 };
 
 // Sequences of one launch: their weights share the memory of two CTAs per SM with the operands, and with the rings

@@ -161,56 +161,62 @@ __device__ __forceinline__ void widen_rows(const uint8_t *src, uint8_t *dst, int
     }
 }
 
-// Row r of the query tile, in place: D bf16 become two rows of D e4m3 codes, q f = q1 + q2 with f a power of two that
-// puts the row's largest magnitude in [2^7, 2^8). q1 keeps four bits, q2 the next four (what is below 2^-10 of q f is
-// lost, 2^-17 of the row's largest). At D = 128 q1 takes the first 128-byte slab and q2 the second; at D = 64 they share
-// the slab's rows. Returns 1 / f (NaN for a row that is not finite: its logits all are).
+// A warp's 32 rows of the query tile, in place: the 64 bf16 of each 128-byte slab row become 64 + 64 e4m3 codes, q f = q1
+// + q2 with f a power of two that puts the row's largest magnitude in [2^7, 2^8). q1 keeps four bits, q2 the next four
+// (what is below 2^-10 of q f is lost: 2^-17 of the row's largest). Eight lanes a row, four rows a step. Returns 1 / f of
+// the lane's own row (NaN for a row that is not finite: its logits all are). A loop, like all that runs once a piece:
+// unrolled, it took 10,000 cycles to fetch.
 template <int D>
-__device__ __forceinline__ float split_query(uint8_t *sq, int r) {
+__device__ __forceinline__ float split_queries(uint8_t *sq, int row0, int lane) {
     constexpr int HALVES = D / 64;
-    uint8_t *row = sq + r * 128;
-    auto at = [&](int hf, int ch) { return reinterpret_cast<uint4 *>(row + hf * (kRows * 128) + ((ch ^ (r & 7)) << 4)); };
-    uint32_t q[HALVES * 32];
+    const int ch = lane & 7;
+    float mine = 1.f;
+#pragma unroll 1
+    for (int step = 0; step < 8; ++step) {
+        const int r = row0 + step * 4 + (lane >> 3);
+        uint8_t *row = sq + r * 128;
+        uint32_t q[HALVES][4];
+        uint32_t top = 0;  // largest magnitude: bf16 magnitudes order like their bits
 #pragma unroll
-    for (int i = 0; i < HALVES * 8; ++i) {
-        const uint4 v = *at(i / 8, i % 8);
-        q[4 * i] = v.x;
-        q[4 * i + 1] = v.y;
-        q[4 * i + 2] = v.z;
-        q[4 * i + 3] = v.w;
-    }
-    uint32_t top = 0;  // largest magnitude: bf16 magnitudes order like their bits
+        for (int hf = 0; hf < HALVES; ++hf) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row + hf * (kRows * 128) + ((ch ^ (r & 7)) << 4));
+            q[hf][0] = v.x;
+            q[hf][1] = v.y;
+            q[hf][2] = v.z;
+            q[hf][3] = v.w;
 #pragma unroll
-    for (int i = 0; i < HALVES * 32; ++i) top = __vmaxu2(top, q[i] & 0x7fff7fffu);
-    const int e = static_cast<int>(max(top & 0xffffu, top >> 16) >> 7);  // exponent field
-    const float f = __uint_as_float(static_cast<uint32_t>(min(261 - e, 247)) << 23);  // 2^(134 - e), at most 2^120
-    uint32_t c1[HALVES * 16], c2[HALVES * 16];
-#pragma unroll
-    for (int i = 0; i < HALVES * 16; ++i) {
-        uint32_t w1 = 0, w2 = 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            float2 v = bf16x2_to_float2(q[2 * i + k]);
-            v = make_float2(v.x * f, v.y * f);
-            const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-            const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(a, __NV_E4M3);
-            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&back));
-            const __nv_fp8x2_storage_t rest =
-                __nv_cvt_float2_to_fp8x2(make_float2(v.x - b.x, v.y - b.y), __NV_SATFINITE, __NV_E4M3);
-            w1 |= static_cast<uint32_t>(a) << (16 * k);
-            w2 |= static_cast<uint32_t>(rest) << (16 * k);
+            for (int i = 0; i < 4; ++i)
+                top = max(top, max(q[hf][i] & 0x7fffu, (q[hf][i] >> 16) & 0x7fffu));
         }
-        c1[i] = w1;
-        c2[i] = w2;
-    }
 #pragma unroll
-    for (int i = 0; i < HALVES * 4; ++i) {
-        const uint4 v1 = make_uint4(c1[4 * i], c1[4 * i + 1], c1[4 * i + 2], c1[4 * i + 3]);
-        const uint4 v2 = make_uint4(c2[4 * i], c2[4 * i + 1], c2[4 * i + 2], c2[4 * i + 3]);
-        *at(0, i) = v1;
-        *(HALVES == 2 ? at(HALVES - 1, i) : at(0, 4 + i)) = v2;
+        for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int e = static_cast<int>(top >> 7);                                                  // exponent field
+        const float f = __uint_as_float(static_cast<uint32_t>(min(261 - e, 247)) << 23);           // 2^(134 - e) or 2^120
+        const float inv = e == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(max(e - 7, 7)) << 23);
+        const float its = __shfl_sync(0xffffffffu, inv, (lane & 3) * 8);
+        if ((lane >> 2) == step) mine = its;
+#pragma unroll
+        for (int hf = 0; hf < HALVES; ++hf) {
+            uint32_t w1[2] = {0, 0}, w2[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 v = bf16x2_to_float2(q[hf][i]);
+                v = make_float2(v.x * f, v.y * f);
+                const __nv_fp8x2_storage_t c1 = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+                const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3);
+                const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+                const __nv_fp8x2_storage_t c2 =
+                    __nv_cvt_float2_to_fp8x2(make_float2(v.x - b.x, v.y - b.y), __NV_SATFINITE, __NV_E4M3);
+                w1[i >> 1] |= static_cast<uint32_t>(c1) << (16 * (i & 1));
+                w2[i >> 1] |= static_cast<uint32_t>(c2) << (16 * (i & 1));
+            }
+            __syncwarp();  // the rows' slabs are read
+            uint8_t *slab = row + hf * (kRows * 128) + (ch & 1) * 8;
+            *reinterpret_cast<uint2 *>(slab + (((ch >> 1) ^ (r & 7)) << 4)) = make_uint2(w1[0], w1[1]);
+            *reinterpret_cast<uint2 *>(slab + (((4 + (ch >> 1)) ^ (r & 7)) << 4)) = make_uint2(w2[0], w2[1]);
+        }
     }
-    return e == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(max(e - 7, 7)) << 23);
+    return mine;
 }
 
 constexpr int kSoftmaxWarps = 4;
@@ -230,7 +236,33 @@ struct TreeBars {
     int abort;
     int arrived;
     int poison[2];
+    int total, ctas;             // weight of the step, CTAs that take a share
+    int bound_prev, bound_next;  // where the share of the CTA before begins and of the CTA after ends
 };
+
+// Waits (bounded) until the four warps of the CTA that came first have stored their partial.
+__device__ __forceinline__ bool wait_stored(const unsigned *count, volatile int *abort, int32_t *status) {
+    bool got = true;
+    if ((threadIdx.x & 31) == 0) {
+        const uint64_t t0 = globaltimer_ns();
+        unsigned seen;
+        for (uint32_t it = 1;; ++it) {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
+            if ((seen >> 4) == kSoftmaxWarps) break;
+            if (*abort) {
+                got = false;
+                break;
+            }
+            if ((it & 63u) == 0 && globaltimer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                atomicOr(status, PKV_STATUS_WAIT_TIMEOUT);
+                got = false;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, got);
+}
 
 template <int D, int BS, bool FP8>
 __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
@@ -356,6 +388,10 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             mbar_init(&B.pv_free[i], 1);
             B.poison[i] = 0;
         }
+        B.total = W;
+        B.ctas = C;
+        B.bound_prev = c > 0 ? static_cast<int>(static_cast<int64_t>(W) * (c - 1) / C) : 0;
+        B.bound_next = c + 2 <= C ? static_cast<int>(static_cast<int64_t>(W) * (c + 2) / C) : W;
         B.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -390,7 +426,8 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
         const bool is_v = warp == kLoadV;
         uint8_t *ring = is_v ? sv : sk;
         uint64_t *full = is_v ? B.v_full : B.k_full, *empty = is_v ? B.v_empty : B.k_empty;
-        const int jb = lane % BPI, hf = lane / BPI;
+        // (a row's slices side by side: with all first slices before all second ones, 8K contexts read 5% slower)
+        const int jb = lane / kSlices, hf = lane % kSlices;
         const bool has = lane < BPI * kSlices;
         auto entry = [&](const Walk &w) {  // this lane's table entry of the iteration, -1: no such block
             const int b = w.it * BPI + jb;
@@ -410,8 +447,13 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             const bool mine = there && p >= 0 && p < a.num_blocks;
             const unsigned m = __ballot_sync(0xffffffffu, mine), lost = __ballot_sync(0xffffffffu, there && !mine);
             if (!is_v) {
-                if (lost && lane == 0) atomicOr(a.status, PKV_STATUS_BAD_BLOCK_ID);
-                if (lane == 0) B.bad[g % kBadRing] = lost & ((1u << BPI) - 1u);
+                uint32_t bits = 0;
+                if (lost) {
+#pragma unroll
+                    for (int k = 0; k < BPI; ++k) bits |= ((lost >> (k * kSlices)) & 1u) << k;
+                    if (lane == 0) atomicOr(a.status, PKV_STATUS_BAD_BLOCK_ID);
+                }
+                if (lane == 0) B.bad[g % kBadRing] = bits;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(__popc(m)) * BS * kRowBytes);
@@ -509,7 +551,7 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                     for (int term = 0; term < 2; ++term)
 #pragma unroll
                         for (int kk = 0; kk < D / 32; ++kk)
-                            umma_f8(tbase, dq + ((term * (HALVES == 2 ? Sh::kQHalf : 64) + kk * 32) >> 4),
+                            umma_f8(tbase, dq + ((kk / 2 * Sh::kQHalf + term * 64 + kk % 2 * 32) >> 4),
                                     dk + ((st * Sh::kTileK + kk * 32) >> 4), instr_desc(128, kTokens, false, true),
                                     (term | kk) != 0);
                 } else {
@@ -601,7 +643,7 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                 // Queries are split by the threads that own them. The head's K scale and the split's factor go into
                 // the logits' factor, V's scale into O.
                 if (!(ok = warp_wait(&B.q_full, piece & 1u, abort_flag, a.status))) break;
-                const float f = a.scale_log2 * __ldg(a.k_scale + walk.h) * (warp_live ? split_query<D>(sq, r) : 1.f);
+                const float f = a.scale_log2 * __ldg(a.k_scale + walk.h) * (warp_live ? split_queries<D>(sq, warp * 32, lane) : 1.f);
                 fence_proxy_async_shared();
                 signal(&B.q_ready);
                 c2 = fabsf(f) < 1e-37f ? 1e-37f : fabsf(f);
@@ -716,8 +758,10 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                     if (!(ok = warp_wait(&B.v_full[st], (g / kStagesV) & 1u, abort_flag, a.status))) break;
                     uint8_t *vt = sv + st * Sh::kTileV;
                     constexpr uint32_t kOdd = FP8 ? 0x7c00u : 0x7f80u;  // exponent of an infinity or a NaN
-                    for (int e = r; e < HALVES * kTokens * 8; e += 128) {
-                        const int hf = e / (kTokens * 8), tok = (e / 8) % kTokens, ch = e % 8;
+                    const int lo = bad ? 0 : max(first - t0, 0);  // rows before are committed tokens
+#pragma unroll 1
+                    for (int e = r; e < HALVES * (kTokens - lo) * 8; e += 128) {
+                        const int tok = lo + e / (HALVES * 8), hf = e / 8 % HALVES, ch = e % 8;
                         uint4 *at = reinterpret_cast<uint4 *>(vt + hf * Sh::kHalfKV + tok * 128 + ((ch ^ (tok & 7)) << 4));
                         if (t0 + tok >= walk.L || ((bad >> (tok / BS)) & 1u)) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
@@ -748,135 +792,127 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                 signal(&B.p_ready[b]);
             }
             if (!ok) break;
-            // ---- the piece's end
+            // ---- the piece's end. Of a segment cut in two, whoever gets here first leaves its partial and goes on; the
+            // other joins the two from its registers (it waits, if at all, for stores already under way).
+            const bool head = walk.it0 == 0, whole = head && walk.it1 == walk.nit;
+            int other = -1;  // the CTA of the other piece, where there are two
+            if (!whole) {
+                const int end = walk.x + walk.nit - walk.it1;  // the segment's end
+                if (head && end <= B.bound_next)
+                    other = c + 1;
+                else if (!head && walk.it1 == walk.nit && walk.x - walk.it1 >= B.bound_prev)
+                    other = c - 1;
+                else if (head && r == 0)
+                    a.cuts[c] = make_int4(walk.q0 + walk.i0, walk.n - walk.i0, walk.h,
+                                          static_cast<int>((static_cast<int64_t>(end) * B.ctas - 1) / B.total) - c + 1);
+            }
+            unsigned *count = a.arrivals + (head ? c : c - 1);
+            if (other >= 0 && r == 0) B.arrived = static_cast<int>(atomicAdd(count, 1u) & 15u);
             if (!(ok = warp_wait(&B.o_full, piece & 1u, abort_flag, a.status))) break;
             tc_fence_after();
             const bool poisoned = poison[piece & 1u] != 0;
-            if (poisoned) {  // cleared for the piece after next once all have read it
-                if (!meet_all()) break;
+            bool join = false;
+            if (other >= 0 || poisoned) {
+                if (!meet_all()) break;  // all know which comes first, and have read the flag
                 if (r == 0) poison[piece & 1u] = 0;
+                join = other >= 0 && *reinterpret_cast<volatile int *>(&B.arrived) != 0;
             }
-            // The CTAs whose shares hold the segment's first and last iteration; a whole segment has one.
-            const int64_t at0 = walk.x - walk.it1, at1 = at0 + walk.nit - 1;  // weight positions of those iterations
-            const int cta0 = a.whole ? c : static_cast<int>(((at0 + 1) * C - 1) / W);
-            const int cta1 = a.whole ? c : static_cast<int>(((at1 + 1) * C - 1) / W);
-            auto partial = [&](int cta) { return (cta * 2 + (cta == cta0 ? 1 : 0)) * static_cast<int64_t>(kRows); };
-            bool store = cta1 > cta0, join = false;
-            if (cta1 == cta0 + 1) {
-                // two pieces: whoever comes second joins them from its registers, and nobody waits
-                unsigned *count = a.arrivals + cta0;
-                if (r == 0) {
-                    unsigned seen;
-                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
-                    B.arrived = static_cast<int>(seen);
-                }
-                if (!meet_all()) break;
-                join = *reinterpret_cast<volatile int *>(&B.arrived) != 0;
-                store = !join;
-            } else if (store && c == cta0 && r == 0) {
-                a.cuts[c] = make_int4(walk.q0 + walk.i0, walk.n - walk.i0, walk.h, cta1 - cta0 + 1);
+            const bool store = !whole && !join;
+            const int64_t own_row = (c * 2 + (head ? 1 : 0)) * static_cast<int64_t>(kRows);
+            const int64_t other_row = (other * 2 + (head ? 0 : 1)) * static_cast<int64_t>(kRows);
+            float scale_mine = l_run == 0.f ? 0.f : 1.f / l_run, scale_other = 0.f;
+            if (join) {
+                if (!(ok = wait_stored(count, abort_flag, a.status))) break;
+                const float2 ml = a.ml_part[other_row + r];
+                const float m = fmaxf(m_ref, ml.x);
+                const float w0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
+                const float w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+                // the same whichever piece comes second: products and sums rounded one by one
+                const float l = __fadd_rn(__fmul_rn(l_run, w0), __fmul_rn(ml.y, w1));
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                scale_mine = w0 * inv;
+                scale_other = w1 * inv;
+            } else if (store && live) {
+                a.ml_part[own_row + r] = make_float2(m_ref, l_run);
             }
-            for (;;) {
-                float scale_mine = l_run == 0.f ? 0.f : 1.f / l_run, scale_other = 0.f;
-                const int64_t own_row = partial(c), other_row = partial(c == cta0 ? cta1 : cta0);
-                if (join) {
-                    const float2 ml = a.ml_part[other_row + r];
-                    const float m = fmaxf(m_ref, ml.x);
-                    const float w0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
-                    const float w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-                    // the same whichever piece comes second: products and sums rounded one by one
-                    const float l = __fadd_rn(__fmul_rn(l_run, w0), __fmul_rn(ml.y, w1));
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    scale_mine = w0 * inv;
-                    scale_other = w1 * inv;
-                } else if (store && live) {
-                    a.ml_part[own_row + r] = make_float2(m_ref, l_run);
-                }
-                if (warp_live) {
+            // a partial is [columns / 4][rows][4]: a warp's rows are side by side
+            float4 *own_part = reinterpret_cast<float4 *>(a.o_part + own_row * D) + r;
+            const float4 *other_part = reinterpret_cast<const float4 *>(a.o_part + other_row * D) + r;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                                 (static_cast<int64_t>(walk.q0 + draft) * a.num_q_heads + walk.h * G + r % G) * D;
+            if (warp_live) {
 #pragma unroll 1
-                    for (int cb = 0; cb < D / 32; ++cb) {
-                        const int col = cb * 32;
-                        float o[32];
-                        tmem_ld32(t_o + col, o);
-                        if (poisoned && live) {
-                            for (int j = max(walk.it0 * kTokens - first, 0); j < min(walk.it1 * kTokens - first, walk.n);
-                                 ++j) {
-                                if (!((bits[j >> 5] >> (j & 31)) & 1)) continue;
-                                const int pos = first + j;
-                                const int p =
-                                    __ldg(a.block_tables + static_cast<int64_t>(walk.s) * a.max_blocks_per_seq + pos / BS);
-                                if (p < 0 || p >= a.num_blocks) continue;
-                                const int64_t at = ((static_cast<int64_t>(p) * BS + pos % BS) * a.num_kv_heads + walk.h) * D + col;
-                                if (FP8) {
-                                    const uint8_t *v = static_cast<const uint8_t *>(a.v_cache) + at;
+                for (int col = 0; col < D; col += 16) {
+                    float4 v[4];
+                    if (join && live) {
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i)
-                                        if ((v[i] & 0x7fu) == 0x7fu) o[i] = NAN;
-                                } else {
-                                    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v_cache) + at;
+                        for (int i = 0; i < 4; ++i) v[i] = other_part[(col / 4 + i) * kRows];
+                    }
+                    float o[16];
+                    tmem_ld16(t_o + col, o);
+                    if (!live) continue;
+                    if (FP8) {
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) {
-                                        const float f = __bfloat162float(v[i]);
-                                        if (!isfinite(f)) o[i] += f;
-                                    }
-                                }
-                            }
+                        for (int i = 0; i < 16; ++i) o[i] *= v_scale;
+                    }
+                    if (store) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            own_part[(col / 4 + i) * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        continue;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __fmul_rn(o[i], scale_mine);
+                    if (join) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            o[4 * i] = __fadd_rn(o[4 * i], __fmul_rn(v[i].x, scale_other));
+                            o[4 * i + 1] = __fadd_rn(o[4 * i + 1], __fmul_rn(v[i].y, scale_other));
+                            o[4 * i + 2] = __fadd_rn(o[4 * i + 2], __fmul_rn(v[i].z, scale_other));
+                            o[4 * i + 3] = __fadd_rn(o[4 * i + 3], __fmul_rn(v[i].w, scale_other));
                         }
-                        if (!live) continue;
-                        if (FP8) {
+                    }
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= v_scale;
+                    for (int i = 0; i < 16; i += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[i + 2 * e], o[i + 2 * e + 1]);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&v2);
                         }
-                        // a partial is [columns / 4][rows][4]: a warp's rows are side by side
-                        if (store) {
-                            float4 *part = reinterpret_cast<float4 *>(a.o_part + own_row * D) + (col / 4) * kRows + r;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                part[i * kRows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                            continue;
-                        }
-                        if (join) {
-                            const float4 *part =
-                                reinterpret_cast<const float4 *>(a.o_part + other_row * D) + (col / 4) * kRows + r;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 v = part[i * kRows];
-                                const float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    o[4 * i + k] = __fadd_rn(__fmul_rn(o[4 * i + k], scale_mine), __fmul_rn(e[k], scale_other));
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= scale_mine;
-                        }
-                        __nv_bfloat16 *dst =
-                            static_cast<__nv_bfloat16 *>(a.out) +
-                            (static_cast<int64_t>(walk.q0 + draft) * a.num_q_heads + walk.h * G + r % G) * D + col;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[i + 2 * e], o[i + 2 * e + 1]);
-                                w[e] = *reinterpret_cast<const uint32_t *>(&v2);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(dst + col + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                if (poisoned && live) {
+                    // the drafts of this piece whose V is not finite, for the rows that see them
+                    const int j1 = min(walk.it1 * kTokens - first, walk.n);
+#pragma unroll 1
+                    for (int j = max(walk.it0 * kTokens - first, 0); j < j1; ++j) {
+                        if (!((bits[j >> 5] >> (j & 31)) & 1)) continue;
+                        const int pos = first + j;
+                        const int p = __ldg(a.block_tables + static_cast<int64_t>(walk.s) * a.max_blocks_per_seq + pos / BS);
+                        if (p < 0 || p >= a.num_blocks) continue;
+                        const int64_t at = ((static_cast<int64_t>(p) * BS + pos % BS) * a.num_kv_heads + walk.h) * D;
+#pragma unroll 1
+                        for (int d = 0; d < D; ++d) {
+                            float f;
+                            if (FP8)
+                                f = (static_cast<const uint8_t *>(a.v_cache)[at + d] & 0x7fu) == 0x7fu ? NAN : 0.f;
+                            else
+                                f = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.v_cache)[at + d]);
+                            if (isfinite(f)) continue;
+                            if (store)
+                                reinterpret_cast<float *>(own_part + d / 4 * kRows)[d % 4] += f;
+                            else
+                                dst[d] = __float2bfloat16(__bfloat162float(dst[d]) + f);
                         }
                     }
                 }
-                if (join || cta1 != cta0 + 1) break;
-                // stored the first of two pieces, or so it seemed: the other may have come meanwhile
+            }
+            if (store && other >= 0) {  // stored: one mark per warp
                 __threadfence();
-                if (!meet_all()) break;
-                if (r == 0) {
-                    B.arrived = static_cast<int>(atomicAdd(a.arrivals + cta0, 1u));
-                    __threadfence();
-                }
-                if (!meet_all()) break;
-                if (*reinterpret_cast<volatile int *>(&B.arrived) == 0) break;
-                store = false;
-                join = true;
+                __syncwarp();
+                if (lane == 0) atomicAdd(count, 16u);
             }
         }
     }
