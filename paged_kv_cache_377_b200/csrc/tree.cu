@@ -924,48 +924,98 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
     }
 }
 
-constexpr int kMergeRows = 32;  // rows of a merge CTA: a lane each
-constexpr int kMergeCols = 8;   // warps: a group of D / 8 columns each
+constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeCols = 32;
+constexpr int kMergeCtas = 296;  // two per SM
 
-// Joins the partials of a segment cut into more than two pieces: out = sum_p O_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).
-// blockIdx.x is the CTA that holds the segment's first piece; the following CTAs' first partials are the others.
-// Also clears the two-piece counters for the next launch.
+// Joins the partials of the segments cut into more than two pieces: out = sum_p O_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).
+// cuts[c] holds the segment that CTA c begins; the following CTAs' first partials are its other pieces. Every CTA lists
+// the segments and takes its share of their (32 rows, 32 columns) items; in an item a lane is a row and a warp every
+// eighth piece, so that 37 pieces of a 32K context are five loads deep. Also clears the two-piece counters for the next
+// launch.
 template <int D>
-__global__ void __launch_bounds__(kMergeRows * kMergeCols) tree_merge_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a, int ctas, int row_chunks) {
+    __shared__ int segments[kTreeMaxCtas];
+    __shared__ unsigned marks[kTreeMaxCtas / 32];
+    __shared__ float2 ml_s[kMergeWarps][32];
+    __shared__ float4 o_s[kMergeWarps][kMergeCols / 4][32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (blockIdx.y == 0 && threadIdx.x == 0) a.arrivals[c] = 0;
-    const int4 cut = a.cuts[c];  // first row's draft, drafts from there on, kv head, pieces
-    const int r = blockIdx.y * kMergeRows + lane;
-    if (r >= min(cut.y, a.tile_drafts) * a.group) return;  // no pieces: no drafts
-    auto partial = [&](int p) { return ((c + p) * 2 + (p == 0 ? 1 : 0)) * static_cast<int64_t>(kRows); };
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int p = 0; p < cut.w; ++p) m = fmaxf(m, a.ml_part[partial(p) + r].x);
-    constexpr int Q = D / 4 / kMergeCols;  // float4 columns per thread
-    float o[4 * Q] = {}, l = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < cut.w; ++p) {
-        const float2 ml = a.ml_part[partial(p) + r];
-        const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-        l += ml.y * w;
-        const float4 *part = reinterpret_cast<const float4 *>(a.o_part + partial(p) * D) + warp * Q * kRows + r;
-#pragma unroll
-        for (int i = 0; i < Q; ++i) {
-            const float4 v = part[i * kRows];
-            o[4 * i] += v.x * w;
-            o[4 * i + 1] += v.y * w;
-            o[4 * i + 2] += v.z * w;
-            o[4 * i + 3] += v.w * w;
-        }
+    for (int k = warp; k < kTreeMaxCtas / 32; k += kMergeWarps) {
+        const int c = k * 32 + lane;
+        const unsigned m = __ballot_sync(0xffffffffu, c < ctas && a.cuts[c].w != 0);
+        if (lane == 0) marks[k] = m;
+        if (blockIdx.x == 0 && c < ctas) a.arrivals[c] = 0;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                         (static_cast<int64_t>(cut.x + r / a.group) * a.num_q_heads + cut.z * a.group + r % a.group) * D +
-                         warp * Q * 4;
+    __syncthreads();
+    int count = 0;  // the list is in the CTAs' order: the same in every merge CTA
 #pragma unroll
-    for (int e = 0; e < 4 * Q; e += 2)
-        *reinterpret_cast<__nv_bfloat162 *>(dst + e) = __floats2bfloat162_rn(o[e] * inv, o[e + 1] * inv);
+    for (int k = 0; k < kTreeMaxCtas / 32; ++k) {
+        if (k % kMergeWarps == warp && (marks[k] >> lane & 1u))
+            segments[count + __popc(marks[k] & ((1u << lane) - 1u))] = k * 32 + lane;
+        count += __popc(marks[k]);
+    }
+    __syncthreads();
+    const int per_segment = row_chunks * (D / kMergeCols), items = count * per_segment;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int c = segments[item / per_segment], rest = item % per_segment;
+        const int r = rest / (D / kMergeCols) * 32 + lane, col = rest % (D / kMergeCols) * kMergeCols;
+        const int4 cut = a.cuts[c];  // first row's draft, drafts from there on, kv head, pieces
+        const bool live = r < min(cut.y, a.tile_drafts) * a.group;
+        auto partial = [&](int p) { return ((c + p) * 2 + (p == 0 ? 1 : 0)) * static_cast<int64_t>(kRows); };
+        float m = -INFINITY, l = 0.f;
+        float4 o[kMergeCols / 4];
+#pragma unroll
+        for (int i = 0; i < kMergeCols / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) {
+#pragma unroll 4
+            for (int p = warp; p < cut.w; p += kMergeWarps) m = fmaxf(m, a.ml_part[partial(p) + r].x);
+#pragma unroll 2
+            for (int p = warp; p < cut.w; p += kMergeWarps) {
+                const float2 ml = a.ml_part[partial(p) + r];
+                const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+                l += ml.y * w;
+                const float4 *part = reinterpret_cast<const float4 *>(a.o_part + partial(p) * D) + col / 4 * kRows + r;
+#pragma unroll
+                for (int i = 0; i < kMergeCols / 4; ++i) {
+                    const float4 v = part[i * kRows];
+                    o[i].x += v.x * w;
+                    o[i].y += v.y * w;
+                    o[i].z += v.z * w;
+                    o[i].w += v.w * w;
+                }
+            }
+        }
+        ml_s[warp][lane] = make_float2(m, l);
+#pragma unroll
+        for (int i = 0; i < kMergeCols / 4; ++i) o_s[warp][i][lane] = o[i];
+        __syncthreads();
+        // warp w joins the eight sums of columns 4 w .. 4 w + 3
+        float top = -INFINITY, sum = 0.f;
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, ml_s[k][lane].x);
+#pragma unroll
+        for (int k = 0; k < kMergeWarps; ++k) {
+            const float2 ml = ml_s[k][lane];
+            const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+            const float4 v = o_s[k][warp][lane];
+            sum += ml.y * w;
+            q.x += v.x * w;
+            q.y += v.y * w;
+            q.z += v.z * w;
+            q.w += v.w * w;
+        }
+        if (live) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(q.x * inv, q.y * inv), hi = __floats2bfloat162_rn(q.z * inv, q.w * inv);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                       (static_cast<int64_t>(cut.x + r / a.group) * a.num_q_heads + cut.z * a.group +
+                                        r % a.group) * D + col + 4 * warp) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        }
+        __syncthreads();
+    }
 }
 
 template <int D, bool FP8>
@@ -985,15 +1035,16 @@ cudaError_t launch(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUten
     if ((e = cudaGetLastError()) != cudaSuccess || a.whole || ctas == 1) return e;
     const int rows = (a.max_query_len < a.tile_drafts ? a.max_query_len : a.tile_drafts) * a.group;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas - 1, (rows + kMergeRows - 1) / kMergeRows);
-    cfg.blockDim = dim3(kMergeRows * kMergeCols);
+    const int row_chunks = (rows + 31) / 32, most = ctas / 2 * row_chunks * (D / kMergeCols);  // three pieces or more each
+    cfg.gridDim = dim3(most < kMergeCtas ? (most > 0 ? most : 1) : kMergeCtas);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a);
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a, ctas, row_chunks);
 }
 
 template <bool FP8>
