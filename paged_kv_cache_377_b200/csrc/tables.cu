@@ -18,47 +18,42 @@ namespace cg = cooperative_groups;
 
 constexpr int kTableThreads = 1024;  // = sequences scanned at a time
 constexpr int kTableWarps = kTableThreads / 32;
+constexpr uint32_t kMany = 0x7fffffffu;  // sums saturate here: more than any pool or step holds
 
-// Exclusive prefix sums of a and b over the CTA's threads; *ta, *tb = totals.
-// `tmp` holds 2 * (kTableWarps + 1) values. Two barriers.
-__device__ __forceinline__ void scan2(int64_t &a, int64_t &b, int64_t *ta, int64_t *tb, int64_t *tmp) {
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, kMany); }  // a, b <= kMany
+
+// Exclusive prefix sums (saturating) of a and b over the CTA's threads; *ta, *tb = totals. Three barriers.
+__device__ __forceinline__ void scan2(uint32_t &a, uint32_t &b, uint32_t *ta, uint32_t *tb, uint2 *tmp) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t xa = a, xb = b;
+    const uint32_t a0 = a, b0 = b;
+    uint32_t xa = a, xb = b;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t ya = __shfl_up_sync(0xffffffffu, xa, d), yb = __shfl_up_sync(0xffffffffu, xb, d);
+        const uint32_t ya = __shfl_up_sync(0xffffffffu, xa, d), yb = __shfl_up_sync(0xffffffffu, xb, d);
         if (lane >= d) {
-            xa += ya;
-            xb += yb;
+            xa = add_sat(xa, ya);
+            xb = add_sat(xb, yb);
         }
     }
     __syncthreads();
-    if (lane == 31) {
-        tmp[warp] = xa;
-        tmp[kTableWarps + warp] = xb;
-    }
+    if (lane == 31) tmp[warp] = make_uint2(xa, xb);
     __syncthreads();
-    int64_t before_a = 0, before_b = 0, all_a = 0, all_b = 0;
-    {
-        int64_t wa = lane < kTableWarps ? tmp[lane] : 0, wb = lane < kTableWarps ? tmp[kTableWarps + lane] : 0;
+    if (warp == 0) {
+        uint2 w = tmp[lane];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t ya = __shfl_up_sync(0xffffffffu, wa, d), yb = __shfl_up_sync(0xffffffffu, wb, d);
-            if (lane >= d) {
-                wa += ya;
-                wb += yb;
-            }
+            const uint32_t ya = __shfl_up_sync(0xffffffffu, w.x, d), yb = __shfl_up_sync(0xffffffffu, w.y, d);
+            if (lane >= d) w = make_uint2(add_sat(w.x, ya), add_sat(w.y, yb));
         }
-        all_a = __shfl_sync(0xffffffffu, wa, 31);
-        all_b = __shfl_sync(0xffffffffu, wb, 31);
-        before_a = __shfl_sync(0xffffffffu, wa, (warp + 31) & 31);
-        before_b = __shfl_sync(0xffffffffu, wb, (warp + 31) & 31);
-        if (warp == 0) before_a = before_b = 0;
+        tmp[lane] = w;
     }
-    a = before_a + xa - a;
-    b = before_b + xb - b;
-    *ta = all_a;
-    *tb = all_b;
+    __syncthreads();
+    const uint2 all = tmp[kTableWarps - 1], before = warp > 0 ? tmp[warp - 1] : make_uint2(0, 0);
+    // inclusive minus own: exact wherever the total is (a saturated one is refused, its parts unused)
+    a = add_sat(before.x, xa) - a0;
+    b = add_sat(before.y, xb) - b0;
+    *ta = all.x;
+    *tb = all.y;
 }
 
 // The last entry of starts[0 .. n) that is <= x (starts[0] = 0 <= x).
@@ -77,21 +72,24 @@ __device__ __forceinline__ int find_start(const int *starts, int n, int x) {
 __device__ __forceinline__ int blocks_of(int tokens, int bs) { return tokens / bs + (tokens % bs != 0); }
 
 struct TableScratch {
-    int64_t scan[2 * (kTableWarps + 1)];
-    int tok[kTableThreads + 1];    // tokens (grow) or freed blocks (trim) before each sequence of the chunk
-    int blk[kTableThreads];        // blocks taken before it
-    int len[kTableThreads];        // its tokens before the call (grow), its first freed entry (trim)
+    uint2 scan[kTableWarps];
+    int tok[kTableThreads];  // tokens (grow) or freed blocks (trim) before each sequence of the chunk
+    int blk[kTableThreads];  // blocks taken before it
+    int len[kTableThreads];  // its tokens before the call (grow), its first freed entry (trim)
     int bad;
 };
 
 // One cluster. Every CTA sums over all sequences (1024 at a time, one thread
 // each), so each knows what the step takes before anything is written: either
-// all of it is given or nothing. New token t of the step is then one thread's:
-// it finds its sequence in the chunk's prefix sums and its block in the table
-// (the tail block the sequence had) or on the stack (the k-th block taken is
-// the k-th from the top); the token that opens a block also writes the table
-// entry. The reads of a chunk's lengths and the writes over them are a cluster
-// barrier apart, so the outputs may be the inputs' own buffers.
+// all of it is given or nothing. With SLOTS, new token t of the step is one
+// thread's: it finds its sequence in the chunk's prefix sums and its block in
+// the table (the tail block the sequence had) or on the stack (the k-th block
+// taken is the k-th from the top); the token that opens a block also writes the
+// table entry. Without (steps of many tokens), a thread per new block writes the
+// table and tables_slots_kernel the slots. The reads of a chunk's lengths and
+// the writes over them are a cluster barrier apart, so the outputs may be the
+// inputs' own buffers.
+template <bool SLOTS>
 __global__ void __launch_bounds__(kTableThreads)
     tables_grow_kernel(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_tokens,
                        const int32_t *free_blocks, const int32_t *num_free, int32_t *new_lens, int32_t *query_start,
@@ -105,76 +103,126 @@ __global__ void __launch_bounds__(kTableThreads)
     if (tid == 0) sm.bad = 0;
     __syncthreads();
 
-    int64_t tokens = 0, blocks = 0;
-    for (int s0 = 0; s0 < num_seqs; s0 += kTableThreads) {
-        const int s = s0 + tid;
-        int64_t n = 0, need = 0, tn, tb;
-        if (s < num_seqs) {
-            const int L = context_lens[s], add = new_tokens[s];
-            if (L < 0 || add < 0 || static_cast<int64_t>(L) + add > cap) {
-                atomicOr(&sm.bad, PKV_STATUS_BAD_CONTEXT_LEN);
-            } else {
-                n = add;
-                need = blocks_of(L + add, block_size) - blocks_of(L, block_size);
-            }
+    int L = 0;
+    uint32_t n = 0, need = 0, tn = 0, tb = 0, tokens = 0, blocks = 0;
+    auto load = [&](int s, bool check) {
+        n = need = 0;
+        if (s >= num_seqs) return;
+        L = context_lens[s];
+        const int add = new_tokens[s];
+        if (L < 0 || add < 0 || static_cast<int64_t>(L) + add > cap) {
+            if (check) atomicOr(&sm.bad, PKV_STATUS_BAD_CONTEXT_LEN);
+            return;
         }
+        n = add;
+        need = blocks_of(L + add, block_size) - blocks_of(L, block_size);
+    };
+    for (int s0 = 0; s0 < num_seqs; s0 += kTableThreads) {
+        load(s0 + tid, true);
+        const uint32_t own_n = n, own_need = need;
         scan2(n, need, &tn, &tb, sm.scan);
-        tokens += tn;
-        blocks += tb;
+        tokens = add_sat(tokens, tn);
+        blocks = add_sat(blocks, tb);
+        if (num_seqs > kTableThreads) {  // scanned again below
+            n = own_n;
+            need = own_need;
+        } else {
+            sm.tok[tid] = static_cast<int>(n);
+            sm.blk[tid] = static_cast<int>(need);
+            n = own_n;
+        }
     }
     __syncthreads();
     int bad = sm.bad;
     if (top < 0 || top > num_blocks)
         bad |= PKV_STATUS_BAD_BLOCK_ID;
-    else if (blocks > top)
+    else if (blocks > static_cast<uint32_t>(top))
         bad |= PKV_STATUS_OUT_OF_BLOCKS;
-    if (tokens > num_slots) bad |= PKV_STATUS_OUT_OF_SLOTS;
+    if (tokens > static_cast<uint32_t>(num_slots)) bad |= PKV_STATUS_OUT_OF_SLOTS;
 
     const int total = bad ? 0 : static_cast<int>(tokens);
-    int64_t tok0 = 0, blk0 = 0;
+    int tok0 = 0, blk0 = 0;
     for (int s0 = 0; s0 < num_seqs; s0 += kTableThreads) {
         const int s = s0 + tid, count = min(kTableThreads, num_seqs - s0);
-        int L = 0;
-        int64_t n = 0, need = 0, tn, tb;
-        if (s < num_seqs) {
-            L = context_lens[s];
-            if (!bad) {
-                n = new_tokens[s];
-                need = blocks_of(L + static_cast<int>(n), block_size) - blocks_of(L, block_size);
-            }
+        int add = static_cast<int>(n);
+        if (num_seqs > kTableThreads) {
+            load(s, false);
+            add = static_cast<int>(n);
+            scan2(n, need, &tn, &tb, sm.scan);
+            sm.tok[tid] = static_cast<int>(n);
+            sm.blk[tid] = static_cast<int>(need);
         }
-        const int add = static_cast<int>(n);
-        scan2(n, need, &tn, &tb, sm.scan);
-        sm.tok[tid] = static_cast<int>(n);
-        sm.blk[tid] = static_cast<int>(blk0 + need);
         sm.len[tid] = L;
         cluster.sync();
         if (rank == 0 && s < num_seqs) {
-            new_lens[s] = L + add;
-            query_start[s + 1] = static_cast<int>(tok0 + n) + add;
+            new_lens[s] = bad ? L : L + add;
+            query_start[s + 1] = bad ? 0 : tok0 + sm.tok[tid] + add;
         }
-        for (int t = rank * kTableThreads + tid; t < tn; t += ctas * kTableThreads) {
-            const int i = find_start(sm.tok, count, t);
-            const int pos = sm.len[i] + t - sm.tok[i];
-            const int lb = pos / block_size, off = pos - lb * block_size;
-            const int have = blocks_of(sm.len[i], block_size);
-            int32_t *entry = block_tables + static_cast<int64_t>(s0 + i) * max_blocks_per_seq + lb;
-            const int p = lb < have ? *entry : free_blocks[top - 1 - (sm.blk[i] + lb - have)];
-            if (lb >= have && off == 0) *entry = p;
-            const bool good = p >= 0 && p < num_blocks;
-            if (!good) atomicOr(status, PKV_STATUS_BAD_BLOCK_ID);
-            slot_mapping[tok0 + t] = good ? static_cast<int64_t>(p) * block_size + off : -1;
+        if (!bad) {
+            const int items = static_cast<int>(SLOTS ? tn : tb);
+            const int *starts = SLOTS ? sm.tok : sm.blk;
+#pragma unroll 4
+            for (int t = rank * kTableThreads + tid; t < items; t += ctas * kTableThreads) {
+                const int i = find_start(starts, count, t);
+                const int have = blocks_of(sm.len[i], block_size);
+                int32_t *row = block_tables + static_cast<int64_t>(s0 + i) * max_blocks_per_seq;
+                if (SLOTS) {
+                    const int pos = sm.len[i] + t - sm.tok[i];
+                    const int lb = pos / block_size, off = pos - lb * block_size;
+                    const int p = lb < have ? row[lb] : free_blocks[top - 1 - (blk0 + sm.blk[i] + lb - have)];
+                    if (lb >= have && off == 0) row[lb] = p;
+                    const bool good = p >= 0 && p < num_blocks;
+                    if (!good) atomicOr(status, PKV_STATUS_BAD_BLOCK_ID);
+                    slot_mapping[tok0 + t] = good ? static_cast<int64_t>(p) * block_size + off : -1;
+                } else {
+                    row[have + t - sm.blk[i]] = free_blocks[top - 1 - (blk0 + t)];
+                }
+            }
         }
-        tok0 += tn;
-        blk0 += tb;
+        tok0 += static_cast<int>(tn);
+        blk0 += static_cast<int>(tb);
         __syncthreads();  // the chunk's arrays are read before the next one's are written
     }
-    for (int64_t t = total + rank * kTableThreads + tid; t < num_slots; t += ctas * kTableThreads) slot_mapping[t] = -1;
+    if (SLOTS)
+        for (int t = total + rank * kTableThreads + tid; t < num_slots; t += ctas * kTableThreads) slot_mapping[t] = -1;
     if (num_seqs == 0) cluster.sync();  // the stack's height was read by every CTA
     if (rank == 0 && tid == 0) {
         query_start[0] = 0;
         *num_free_out = bad ? top : top - static_cast<int>(blocks);
         if (bad) atomicOr(status, bad);
+    }
+}
+
+constexpr int kSlotThreads = 256, kSlotSeqs = 8192;  // starts kept in shared memory
+
+// The slots of a step of many tokens, from the lengths, starts and tables that tables_grow_kernel<false> wrote: a
+// thread per token, over the whole device (the grow kernel's one cluster took 41 us for 256,000 tokens).
+__global__ void __launch_bounds__(kSlotThreads)
+    tables_slots_kernel(const int32_t *block_tables, const int32_t *new_lens, const int32_t *query_start,
+                        int64_t *slot_mapping, int num_seqs, int num_slots, int max_blocks_per_seq, int block_size,
+                        int num_blocks, int32_t *status) {
+    extern __shared__ int kept[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int *starts = query_start;
+    if (num_seqs <= kSlotSeqs) {
+        for (int s = threadIdx.x; s <= num_seqs; s += kSlotThreads) kept[s] = query_start[s];
+        __syncthreads();
+        starts = kept;
+    }
+    const int total = starts[num_seqs], step = gridDim.x * kSlotThreads;
+#pragma unroll 4
+    for (int t = blockIdx.x * kSlotThreads + threadIdx.x; t < num_slots; t += step) {
+        int64_t slot = -1;
+        if (t < total) {
+            const int s = find_start(starts, num_seqs, t);
+            const int pos = new_lens[s] - (starts[s + 1] - t);
+            const int p = block_tables[static_cast<int64_t>(s) * max_blocks_per_seq + pos / block_size];
+            if (p >= 0 && p < num_blocks)
+                slot = static_cast<int64_t>(p) * block_size + pos % block_size;
+            else
+                atomicOr(status, PKV_STATUS_BAD_BLOCK_ID);
+        }
+        slot_mapping[t] = slot;
     }
 }
 
@@ -192,44 +240,47 @@ __global__ void __launch_bounds__(kTableThreads)
     if (tid == 0) sm.bad = 0;
     __syncthreads();
 
-    int64_t freed = 0;
-    for (int s0 = 0; s0 < num_seqs; s0 += kTableThreads) {
-        const int s = s0 + tid;
-        int64_t gone = 0, zero = 0, tg, tz;
-        if (s < num_seqs) {
-            const int L = context_lens[s], keep = keep_lens[s];
-            if (keep < 0 || keep > L || L > cap)
-                atomicOr(&sm.bad, PKV_STATUS_BAD_CONTEXT_LEN);
-            else
-                gone = blocks_of(L, block_size) - blocks_of(keep, block_size);
+    int first = 0;
+    uint32_t gone = 0, zero = 0, tg = 0, tz = 0, sum = 0;
+    auto load = [&](int s, bool check) {
+        gone = zero = 0;
+        if (s >= num_seqs) return;
+        const int L = context_lens[s], keep = keep_lens[s];
+        if (keep < 0 || keep > L || L > cap) {
+            if (check) atomicOr(&sm.bad, PKV_STATUS_BAD_CONTEXT_LEN);
+            return;
         }
+        first = blocks_of(keep, block_size);
+        gone = blocks_of(L, block_size) - first;
+    };
+    for (int s0 = 0; s0 < num_seqs; s0 += kTableThreads) {
+        load(s0 + tid, true);
         scan2(gone, zero, &tg, &tz, sm.scan);
-        freed += tg;
+        sum = add_sat(sum, tg);
     }
     __syncthreads();
     int bad = sm.bad;
-    if (top < 0 || top + freed > num_blocks) bad |= PKV_STATUS_BAD_BLOCK_ID;
+    if (top < 0 || top > num_blocks || sum > static_cast<uint32_t>(num_blocks - top)) bad |= PKV_STATUS_BAD_BLOCK_ID;
     cluster.sync();  // every CTA has read the stack's height
+    const int freed = static_cast<int>(sum);
     if (rank == 0 && tid == 0) {
-        *num_free_out = bad ? top : top + static_cast<int>(freed);
+        *num_free_out = bad ? top : top + freed;
         if (bad) atomicOr(status, bad);
     }
     if (bad) return;
 
-    int64_t done = 0;
+    int done = 0;
     for (int s0 = 0; s0 < num_seqs; s0 += kTableThreads) {
-        const int s = s0 + tid, count = min(kTableThreads, num_seqs - s0);
-        int64_t gone = 0, zero = 0, tg, tz;
-        int first = 0;
-        if (s < num_seqs) {
-            first = blocks_of(keep_lens[s], block_size);
-            gone = blocks_of(context_lens[s], block_size) - first;
+        const int count = min(kTableThreads, num_seqs - s0);
+        if (num_seqs > kTableThreads) {
+            load(s0 + tid, false);
+            scan2(gone, zero, &tg, &tz, sm.scan);
         }
-        scan2(gone, zero, &tg, &tz, sm.scan);
         sm.tok[tid] = static_cast<int>(gone);
         sm.len[tid] = first;
         __syncthreads();
-        for (int k = rank * kTableThreads + tid; k < tg; k += ctas * kTableThreads) {
+#pragma unroll 4
+        for (int k = rank * kTableThreads + tid; k < static_cast<int>(tg); k += ctas * kTableThreads) {
             const int i = find_start(sm.tok, count, k);
             int p = block_tables[static_cast<int64_t>(s0 + i) * max_blocks_per_seq + sm.len[i] + k - sm.tok[i]];
             if (p < 0 || p >= num_blocks) {
@@ -238,43 +289,63 @@ __global__ void __launch_bounds__(kTableThreads)
             }
             free_blocks[top + freed - 1 - (done + k)] = p;
         }
-        done += tg;
+        done += static_cast<int>(tg);
         __syncthreads();
     }
 }
 
-// One CTA per sequence, a thread per node: it walks up the tree. Ancestors are
-// earlier nodes, so the walk meets the row's words from the last to the first
-// and each is written once.
-__global__ void __launch_bounds__(128)
+constexpr int kMaskThreads = 128;
+
+// One CTA per sequence. Within a run of 32 nodes a warp closes the tree by
+// pointer doubling: lane i gets the bits of its ancestors in the run, and the
+// lowest of them leads out of it (ancestors are earlier nodes). A thread per
+// node then hops from run to run, one mask word each, from the last to the
+// first: at most n / 32 steps, where a walk from parent to parent took n (a
+// chain of 256: 58 us).
+__global__ void __launch_bounds__(kMaskThreads)
     tree_mask_kernel(int32_t *tree_mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
                      int num_tokens, int max_query_len, int mask_words, int32_t *status) {
-    extern __shared__ int up[];
-    const int s = blockIdx.x, tid = threadIdx.x;
+    extern __shared__ int2 runs[];  // per node: its run's bits, the node that its run's topmost ancestor hangs from
+    const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const int q0 = query_start[s], q1 = query_start[s + 1], n = q1 - q0;
     if (q0 < 0 || n < 0 || q1 > num_tokens || n > max_query_len) {
         if (tid == 0) atomicOr(status, PKV_STATUS_BAD_CONTEXT_LEN);
         return;
     }
-    for (int i = tid; i < n; i += blockDim.x) {
-        int p = parents[q0 + i];
-        if (p < -1 || p >= i) {
+    for (int i0 = tid - lane; i0 < n; i0 += kMaskThreads) {
+        const int i = i0 + lane;
+        int up = i < n ? parents[q0 + i] : -1;
+        if (up < -1 || up >= i) {
             atomicOr(status, PKV_STATUS_BAD_TREE);
-            p = -1;
+            up = -1;
         }
-        up[i] = p;
+        uint32_t bits = 1u << lane;
+        int jump = up >= i0 ? up - i0 : -1;  // an ancestor in the run
+#pragma unroll
+        for (int d = 0; d < 5; ++d) {
+            const int from = jump < 0 ? lane : jump;
+            const uint32_t more = __shfl_sync(0xffffffffu, bits, from);
+            const int next = __shfl_sync(0xffffffffu, jump, from);
+            if (jump >= 0) {
+                bits |= more;
+                jump = next;
+            }
+        }
+        const int out = __shfl_sync(0xffffffffu, up, __ffs(bits) - 1);
+        if (i < n) runs[i] = make_int2(static_cast<int>(bits), out);
     }
     __syncthreads();
-    for (int i = tid; i < n; i += blockDim.x) {
+    for (int i = tid; i < n; i += kMaskThreads) {
         int32_t *row = tree_mask + static_cast<int64_t>(q0 + i) * mask_words;
         int w = mask_words - 1, depth = -1;
-        uint32_t word = 0;
-        for (int j = i; j >= 0; j = up[j]) {
-            for (; w > (j >> 5); --w, word = 0) row[w] = static_cast<int32_t>(word);
-            word |= 1u << (j & 31);
-            ++depth;
+        for (int j = i; j >= 0;) {
+            const int2 run = runs[j];
+            for (; w > (j >> 5); --w) row[w] = 0;
+            row[w--] = run.x;
+            depth += __popc(static_cast<uint32_t>(run.x));
+            j = run.y;
         }
-        for (; w >= 0; --w, word = 0) row[w] = static_cast<int32_t>(word);
+        for (; w >= 0; --w) row[w] = 0;
         depths[q0 + i] = depth;
     }
 }
@@ -372,6 +443,9 @@ cudaLaunchConfig_t table_config(int ctas, cudaLaunchAttribute *attr, cudaStream_
     return cfg;
 }
 
+// Steps of more slots than this leave them to tables_slots_kernel.
+constexpr int kClusterSlots = 16384;
+
 }  // namespace
 
 cudaError_t tables_grow_launch(int32_t *block_tables, const int32_t *context_lens, const int32_t *new_tokens,
@@ -380,10 +454,22 @@ cudaError_t tables_grow_launch(int32_t *block_tables, const int32_t *context_len
                                int num_slots, int max_blocks_per_seq, int block_size, int num_blocks, int32_t *status,
                                cudaStream_t stream) {
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = table_config(table_ctas(num_slots), &attr, stream);
-    return cudaLaunchKernelEx(&cfg, tables_grow_kernel, block_tables, context_lens, new_tokens, free_blocks, num_free,
-                              new_lens, query_start, slot_mapping, num_free_out, num_seqs, num_slots,
-                              max_blocks_per_seq, block_size, num_blocks, status);
+    const bool few = num_slots <= kClusterSlots;
+    cudaLaunchConfig_t cfg = table_config(table_ctas(few ? num_slots : num_slots / block_size + num_seqs), &attr, stream);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, few ? tables_grow_kernel<true> : tables_grow_kernel<false>, block_tables,
+                                       context_lens, new_tokens, free_blocks, num_free, new_lens, query_start,
+                                       slot_mapping, num_free_out, num_seqs, num_slots, max_blocks_per_seq, block_size,
+                                       num_blocks, status);
+    if (e != cudaSuccess || few) return e;
+    const int blocks = (num_slots + kSlotThreads - 1) / kSlotThreads;
+    cfg.gridDim = dim3(blocks < 148 * 8 ? blocks : 148 * 8);
+    cfg.blockDim = dim3(kSlotThreads);
+    cfg.dynamicSmemBytes = num_seqs <= kSlotSeqs ? (static_cast<size_t>(num_seqs) + 1) * 4 : 0;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, tables_slots_kernel, static_cast<const int32_t *>(block_tables),
+                              static_cast<const int32_t *>(new_lens), static_cast<const int32_t *>(query_start),
+                              slot_mapping, num_seqs, num_slots, max_blocks_per_seq, block_size, num_blocks, status);
 }
 
 cudaError_t tables_trim_launch(const int32_t *block_tables, const int32_t *context_lens, const int32_t *keep_lens,
@@ -400,7 +486,7 @@ cudaError_t tables_trim_launch(const int32_t *block_tables, const int32_t *conte
 cudaError_t tree_mask_launch(int32_t *tree_mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
                              int num_seqs, int num_tokens, int max_query_len, int mask_words, int32_t *status,
                              cudaStream_t stream) {
-    tree_mask_kernel<<<num_seqs, 128, static_cast<size_t>(max_query_len) * 4, stream>>>(
+    tree_mask_kernel<<<num_seqs, kMaskThreads, static_cast<size_t>(max_query_len) * 8, stream>>>(
         tree_mask, depths, parents, query_start, num_tokens, max_query_len, mask_words, status);
     return cudaGetLastError();
 }
