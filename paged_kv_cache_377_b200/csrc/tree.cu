@@ -925,20 +925,20 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
 }
 
 constexpr int kMergeThreads = 256, kMergeWarps = kMergeThreads / 32;
-constexpr int kMergeCols = 32;
+constexpr int kMergeCols = 16, kMergeQuads = kMergeCols / 4;
 constexpr int kMergeCtas = 296;  // two per SM
 
 // Joins the partials of the segments cut into more than two pieces: out = sum_p O_p 2^(m_p - m) / sum_p l_p 2^(m_p - m).
 // cuts[c] holds the segment that CTA c begins; the following CTAs' first partials are its other pieces. Every CTA lists
-// the segments and takes its share of their (32 rows, 32 columns) items; in an item a lane is a row and a warp every
-// eighth piece, so that 37 pieces of a 32K context are five loads deep. Also clears the two-piece counters for the next
-// launch.
+// the segments and takes its share of their (32 rows, 16 columns) items; in an item a lane is a row and a warp every
+// eighth piece, four of which it loads at once: the 37 pieces of a 32K context are two round trips. Also clears the
+// two-piece counters for the next launch.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArgs a, int ctas, int row_chunks) {
     __shared__ int segments[kTreeMaxCtas];
     __shared__ unsigned marks[kTreeMaxCtas / 32];
     __shared__ float2 ml_s[kMergeWarps][32];
-    __shared__ float4 o_s[kMergeWarps][kMergeCols / 4][32];
+    __shared__ float4 o_s[kMergeWarps][kMergeQuads][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int k = warp; k < kTreeMaxCtas / 32; k += kMergeWarps) {
@@ -964,33 +964,48 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
         const bool live = r < min(cut.y, a.tile_drafts) * a.group;
         auto partial = [&](int p) { return ((c + p) * 2 + (p == 0 ? 1 : 0)) * static_cast<int64_t>(kRows); };
         float m = -INFINITY, l = 0.f;
-        float4 o[kMergeCols / 4];
+        float4 o[kMergeQuads];
 #pragma unroll
-        for (int i = 0; i < kMergeCols / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < kMergeQuads; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live) {
-#pragma unroll 4
-            for (int p = warp; p < cut.w; p += kMergeWarps) m = fmaxf(m, a.ml_part[partial(p) + r].x);
-#pragma unroll 2
-            for (int p = warp; p < cut.w; p += kMergeWarps) {
-                const float2 ml = a.ml_part[partial(p) + r];
-                const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-                l += ml.y * w;
-                const float4 *part = reinterpret_cast<const float4 *>(a.o_part + partial(p) * D) + col / 4 * kRows + r;
+            for (int p0 = warp; p0 < cut.w; p0 += 4 * kMergeWarps) {
+                float2 ml[4];
+                float4 v[4][kMergeQuads];
 #pragma unroll
-                for (int i = 0; i < kMergeCols / 4; ++i) {
-                    const float4 v = part[i * kRows];
-                    o[i].x += v.x * w;
-                    o[i].y += v.y * w;
-                    o[i].z += v.z * w;
-                    o[i].w += v.w * w;
+                for (int k = 0; k < 4; ++k) {
+                    const int p = p0 + k * kMergeWarps;
+                    if (p >= cut.w) break;
+                    ml[k] = a.ml_part[partial(p) + r];
+                    const float4 *part = reinterpret_cast<const float4 *>(a.o_part + partial(p) * D) + col / 4 * kRows + r;
+#pragma unroll
+                    for (int i = 0; i < kMergeQuads; ++i) v[k][i] = part[i * kRows];
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (p0 + k * kMergeWarps >= cut.w) break;
+                    const float top = fmaxf(m, ml[k].x);
+                    const float keep = m == -INFINITY ? 0.f : fast_exp2(m - top);
+                    const float w = ml[k].x == -INFINITY ? 0.f : fast_exp2(ml[k].x - top);
+                    m = top;
+                    l = l * keep + ml[k].y * w;
+#pragma unroll
+                    for (int i = 0; i < kMergeQuads; ++i) {
+                        o[i].x = o[i].x * keep + v[k][i].x * w;
+                        o[i].y = o[i].y * keep + v[k][i].y * w;
+                        o[i].z = o[i].z * keep + v[k][i].z * w;
+                        o[i].w = o[i].w * keep + v[k][i].w * w;
+                    }
                 }
             }
         }
         ml_s[warp][lane] = make_float2(m, l);
 #pragma unroll
-        for (int i = 0; i < kMergeCols / 4; ++i) o_s[warp][i][lane] = o[i];
+        for (int i = 0; i < kMergeQuads; ++i) o_s[warp][i][lane] = o[i];
         __syncthreads();
-        // warp w joins the eight sums of columns 4 w .. 4 w + 3
+        if (warp >= kMergeQuads) {  // warp w < 4 joins the eight sums of columns 4 w .. 4 w + 3
+            __syncthreads();
+            continue;
+        }
         float top = -INFINITY, sum = 0.f;
         float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

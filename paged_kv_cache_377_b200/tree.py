@@ -58,10 +58,13 @@ def _pointers(*specs):
     return out
 
 
+# the current stream's handle, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream, device: int):
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return b._stream(stream)
+    return _raw_stream(device) if stream is None else b._stream(stream)
 
 
 def tree_workspace_bytes(head_dim: int) -> int:
