@@ -284,6 +284,43 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
     TreeBars &B = *reinterpret_cast<TreeBars *>(raw + Sh::kRaw);
     int *wp = reinterpret_cast<int *>(&B + 1);
 
+    // ---- barriers and tensor memory, while the lengths are on their way
+    if (warp == kMma) {  // all of the CTA's columns
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
+        tc_fence_before();
+    } else if (warp == kLoadK && lane == 0) {
+        mbar_init(&B.q_full, 1);
+        mbar_init(&B.q_empty, 1);
+        mbar_init(&B.done, 1);
+        mbar_init(&B.s_full, 1);
+        mbar_init(&B.s_free, kSoftmaxWarps);
+        mbar_init(&B.o_full, 1);
+        mbar_init(&B.all, kSoftmaxWarps);
+        mbar_init(&B.q_ready, kSoftmaxWarps);
+        for (int i = 0; i < kStagesK; ++i) {
+            mbar_init(&B.k_full[i], 1);
+            mbar_init(&B.k_empty[i], 1);
+        }
+        for (int i = 0; i < kStagesV; ++i) {
+            mbar_init(&B.v_full[i], FP8 ? 2 : 1);
+            mbar_init(&B.v_empty[i], 1);
+            mbar_init(&B.raw_full[0][i], 1);
+            mbar_init(&B.raw_full[1][i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B.p_ready[i], kSoftmaxWarps);
+            mbar_init(&B.pv_free[i], 1);
+            B.poison[i] = 0;
+        }
+        B.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+
     // ---- weights: every CTA sums over all sequences (one contiguous run per thread)
     const int entries = a.num_seqs * a.lists;
     {
@@ -343,10 +380,26 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
     const int W = wp[entries];
     const int C = min(static_cast<int>(gridDim.x), W / a.min_weight + (W % a.min_weight != 0));  // CTAs that take a share
     const int c = blockIdx.x;
-    if (c >= C) return;
+    auto share = [&](int k) {  // where CTA k's share begins (a 32-bit division where the product fits)
+        return W <= 0x7fffffff / kTreeMaxCtas ? static_cast<int>(static_cast<uint32_t>(W) * k / static_cast<uint32_t>(C))
+                                              : static_cast<int>(static_cast<int64_t>(W) * k / C);
+    };
+    if (c >= C) {
+        if (warp == kMma) {
+            tc_fence_after();
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(B.tmem), "r"(kTmemCols));
+        }
+        return;
+    }
     Walk walk;
-    walk.x = static_cast<int>(static_cast<int64_t>(W) * c / C);
-    walk.x1 = static_cast<int>(static_cast<int64_t>(W) * (c + 1) / C);
+    walk.x = share(c);
+    walk.x1 = share(c + 1);
+    if (tid == 0) {
+        B.total = W;
+        B.ctas = C;
+        B.bound_prev = c > 0 ? share(c - 1) : 0;
+        B.bound_next = c + 2 <= C ? share(c + 2) : W;
+    }
     {
         int lo = 0, hi = entries;  // wp[lo] <= x < wp[hi]
         while (hi - lo > 1) {
@@ -357,46 +410,6 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                 hi = mid;
         }
         walk.e = lo;
-    }
-
-    if (warp == kMma) {  // all of the CTA's columns
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)),
-                     "r"(kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::);
-        tc_fence_before();
-    } else if (warp == kLoadK && lane == 0) {
-        mbar_init(&B.q_full, 1);
-        mbar_init(&B.q_empty, 1);
-        mbar_init(&B.done, 1);
-        mbar_init(&B.s_full, 1);
-        mbar_init(&B.s_free, kSoftmaxWarps);
-        mbar_init(&B.o_full, 1);
-        mbar_init(&B.all, kSoftmaxWarps);
-        mbar_init(&B.q_ready, kSoftmaxWarps);
-        for (int i = 0; i < kStagesK; ++i) {
-            mbar_init(&B.k_full[i], 1);
-            mbar_init(&B.k_empty[i], 1);
-        }
-        for (int i = 0; i < kStagesV; ++i) {
-            mbar_init(&B.v_full[i], FP8 ? 2 : 1);
-            mbar_init(&B.v_empty[i], 1);
-            mbar_init(&B.raw_full[0][i], 1);
-            mbar_init(&B.raw_full[1][i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&B.p_ready[i], kSoftmaxWarps);
-            mbar_init(&B.pv_free[i], 1);
-            B.poison[i] = 0;
-        }
-        B.total = W;
-        B.ctas = C;
-        B.bound_prev = c > 0 ? static_cast<int>(static_cast<int64_t>(W) * (c - 1) / C) : 0;
-        B.bound_next = c + 2 <= C ? static_cast<int>(static_cast<int64_t>(W) * (c + 2) / C) : W;
-        B.abort = 0;
-        fence_mbar_init();
-        tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
     }
     __syncthreads();
     tc_fence_after();
@@ -808,22 +821,22 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             }
             unsigned *count = a.arrivals + (head ? c : c - 1);
             if (other >= 0 && r == 0) B.arrived = static_cast<int>(atomicAdd(count, 1u) & 15u);
-            if (!(ok = warp_wait(&B.o_full, piece & 1u, abort_flag, a.status))) break;
-            tc_fence_after();
-            const bool poisoned = poison[piece & 1u] != 0;
             bool join = false;
-            if (other >= 0 || poisoned) {
-                if (!meet_all()) break;  // all know which comes first, and have read the flag
-                if (r == 0) poison[piece & 1u] = 0;
-                join = other >= 0 && *reinterpret_cast<volatile int *>(&B.arrived) != 0;
+            if (other >= 0) {
+                if (!meet_all()) break;  // all know which comes first
+                join = *reinterpret_cast<volatile int *>(&B.arrived) != 0;
             }
             const bool store = !whole && !join;
             const int64_t own_row = (c * 2 + (head ? 1 : 0)) * static_cast<int64_t>(kRows);
             const int64_t other_row = (other * 2 + (head ? 0 : 1)) * static_cast<int64_t>(kRows);
+            const float4 *other_part = reinterpret_cast<const float4 *>(a.o_part + other_row * D) + r;
             float scale_mine = l_run == 0.f ? 0.f : 1.f / l_run, scale_other = 0.f;
+            float4 v[4];  // the other piece's next 16 columns, asked for ahead (one by one, they took 12,000 cycles)
             if (join) {
                 if (!(ok = wait_stored(count, abort_flag, a.status))) break;
                 const float2 ml = a.ml_part[other_row + r];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = other_part[i * kRows];
                 const float m = fmaxf(m_ref, ml.x);
                 const float w0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
                 const float w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
@@ -835,19 +848,20 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             } else if (store && live) {
                 a.ml_part[own_row + r] = make_float2(m_ref, l_run);
             }
+            if (!(ok = warp_wait(&B.o_full, piece & 1u, abort_flag, a.status))) break;
+            tc_fence_after();
+            const bool poisoned = poison[piece & 1u] != 0;
+            if (poisoned) {
+                if (!meet_all()) break;  // all have read the flag
+                if (r == 0) poison[piece & 1u] = 0;
+            }
             // a partial is [columns / 4][rows][4]: a warp's rows are side by side
             float4 *own_part = reinterpret_cast<float4 *>(a.o_part + own_row * D) + r;
-            const float4 *other_part = reinterpret_cast<const float4 *>(a.o_part + other_row * D) + r;
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
                                  (static_cast<int64_t>(walk.q0 + draft) * a.num_q_heads + walk.h * G + r % G) * D;
             if (warp_live) {
 #pragma unroll 1
                 for (int col = 0; col < D; col += 16) {
-                    float4 v[4];
-                    if (join && live) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = other_part[(col / 4 + i) * kRows];
-                    }
                     float o[16];
                     tmem_ld16(t_o + col, o);
                     if (!live) continue;
@@ -870,6 +884,10 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                             o[4 * i + 1] = __fadd_rn(o[4 * i + 1], __fmul_rn(v[i].y, scale_other));
                             o[4 * i + 2] = __fadd_rn(o[4 * i + 2], __fmul_rn(v[i].z, scale_other));
                             o[4 * i + 3] = __fadd_rn(o[4 * i + 3], __fmul_rn(v[i].w, scale_other));
+                        }
+                        if (col + 16 < D) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] = other_part[((col + 16) / 4 + i) * kRows];
                         }
                     }
 #pragma unroll
