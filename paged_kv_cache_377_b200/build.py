@@ -1,4 +1,5 @@
-"""Builds libpagedkv.so in-tree with nvcc for sm_100a.
+"""Builds libpagedkv.so in-tree with nvcc for sm_100a, and beside it _marshal.so
+(csrc/marshal.cpp: the Python side of the small calls, against torch's headers).
 
 ``python -m paged_kv_cache_377_b200.build`` or ``build()``; each translation
 unit compiles in parallel into ``_build/`` and is linked into
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 SOURCES = ["api.cu", "decode.cu", "append.cu", "selftest.cu", "block_manager.cu", "prefill.cu", "prefill_tc.cu",
            "tree.cu", "tables.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -39,9 +41,9 @@ def _inputs() -> List[str]:
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -61,14 +63,41 @@ def build(force: bool = False, verbose: bool = False, extra_flags: List[str] = (
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_marshal() -> str:
+        import sysconfig
+
+        import torch
+        from torch.utils import cpp_extension
+        obj = os.path.join(BUILD, "marshal.o")
+        include = [a for d in [INCLUDE, *cpp_extension.include_paths(), os.path.join(os.path.dirname(cc), "..", "include"),
+                               sysconfig.get_path("include")] for a in ("-I", d)]
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *include, "-c",
+               os.path.join(CSRC, "marshal.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on marshal.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(compile_marshal)
         objs = list(ex.map(compile_one, SOURCES))
+        marshal_obj = marshal.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
+    cmd = [cc, *ARCH, "-shared", "-Xlinker", "-soname,libpagedkv.so", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-shared", "-o", tmp, marshal_obj, LIB, "-L", lib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
     return LIB
 
 

@@ -439,7 +439,7 @@ cudaLaunchConfig_t table_config(int ctas, cudaLaunchAttribute *attr, cudaStream_
     attr->val.clusterDim.y = 1;
     attr->val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1 ? 1 : 0;  // a launch without the attribute is a cluster of one, and sooner made
     return cfg;
 }
 
@@ -467,6 +467,7 @@ cudaError_t tables_grow_launch(int32_t *block_tables, const int32_t *context_len
     cfg.dynamicSmemBytes = num_seqs <= kSlotSeqs ? (static_cast<size_t>(num_seqs) + 1) * 4 : 0;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, tables_slots_kernel, static_cast<const int32_t *>(block_tables),
                               static_cast<const int32_t *>(new_lens), static_cast<const int32_t *>(query_start),
                               slot_mapping, num_seqs, num_slots, max_blocks_per_seq, block_size, num_blocks, status);

@@ -33,6 +33,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "device_utils.cuh"
 #include "launch.h"
 #include "tcgen05_utils.cuh"
@@ -1062,8 +1064,17 @@ cudaError_t launch(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUten
                    int ctas, cudaStream_t stream) {
     const size_t smem = tree_smem_bytes<D, FP8>(a.num_seqs * a.lists);
     auto *fn = paged_tree_kernel<D, BS, FP8>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> prepared{0};  // devices whose limit is set, to the largest that a launch asks for
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev > 63 || !(prepared.load() & bit)) {
+        const size_t most = tree_smem_bytes<D, FP8>(2 * (FP8 ? kTreeMaxSeqsFp8 : kTreeMaxSeqs));
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+        if (e != cudaSuccess) return e;
+        prepared |= bit;
+    }
     fn<<<ctas, TreeShape<D, FP8>::kThreads, smem, stream>>>(tm_q, tm_k, tm_v, a);
     if ((e = cudaGetLastError()) != cudaSuccess || a.whole || ctas == 1) return e;
     const int rows = (a.max_query_len < a.tile_drafts ? a.max_query_len : a.tile_drafts) * a.group;
