@@ -873,6 +873,7 @@ int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const voi
         int64_t ctas = 2 * static_cast<int64_t>(sms);
         if (ctas > pkv::kTreeMaxCtas) ctas = pkv::kTreeMaxCtas;
         if (ctas > bound) ctas = bound;
+        if (a.lists == 2 && ctas < 3) ctas = 3;  // pairs' first tiles, second tiles, and single ones
         const cudaError_t e = pkv::tree_launch(fp8, head_dim, tm_q, tm_k, tm_v, a, static_cast<int>(ctas),
                                                static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
