@@ -241,6 +241,7 @@ struct TreeBars {
     int abort;
     int arrived;
     int poison[2];
+    Walk walk[4];  // the softmax warps' pieces
     int start, total, ctas, index;  // the CTA's group: weight positions, CTAs, and its own place among them
     int bound_prev, bound_next;     // where the share of the CTA before begins and of the CTA after ends
 };
@@ -666,26 +667,36 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             signal(&B.all);
             return ok = warp_wait(&B.all, met_all++ & 1u, abort_flag, a.status);
         };
-        while (ok && walk.next_piece(a, wp)) {
+        // the piece that is worked on lives in shared memory, a copy per warp: only what the loop needs takes registers
+        Walk &now = B.walk[warp];
+        if (lane == 0) now = walk;
+        __syncwarp();
+        while (ok) {
+            Walk next = now;
+            const bool more = next.next_piece(a, wp);
+            __syncwarp();
+            if (lane == 0) now = next;
+            __syncwarp();
+            if (!more) break;
             const uint32_t piece = pieces++;
-            const int draft = walk.i0 + r / G;
-            const bool live = !spare && draft < walk.n;
+            const int it0 = next.it0, it1 = next.it1, first = next.L - next.n;  // first draft's position
+            const int draft = next.i0 + r / G;
+            const bool live = !spare && draft < next.n;
             const bool warp_live = __any_sync(0xffffffffu, live);
             if (FP8) {
                 // Queries are split by the threads that own them. The head's K scale and the split's factor go into
                 // the logits' factor, V's scale into O.
                 if (!(ok = warp_wait(&B.q_full, piece & 1u, abort_flag, a.status))) break;
-                const float f = a.scale_log2 * __ldg(a.k_scale + walk.h) * (warp_live ? split_queries<D>(sq, warp * 32, lane) : 1.f);
+                const float f = a.scale_log2 * __ldg(a.k_scale + next.h) * (warp_live ? split_queries<D>(sq, warp * 32, lane) : 1.f);
                 fence_proxy_async_shared();
                 signal(&B.q_ready);
                 c2 = fabsf(f) < 1e-37f ? 1e-37f : fabsf(f);
                 negative = f < 0.f;
-                v_scale = __ldg(a.v_scale + walk.h);
+                v_scale = __ldg(a.v_scale + next.h);
             }
-            const int first = walk.L - walk.n;  // first draft's position
-            const int32_t *bits = a.tree_mask + static_cast<int64_t>(walk.q0 + min(draft, walk.n - 1)) * a.mask_words;
+            const int32_t *bits = a.tree_mask + static_cast<int64_t>(next.q0 + min(draft, next.n - 1)) * a.mask_words;
             float m_ref = -INFINITY, l_run = 0.f;
-            for (int it = walk.it0; it < walk.it1; ++it, ++g) {
+            for (int it = it0; it < it1; ++it, ++g) {
                 const uint32_t b = g & 1u;
                 const int t0 = it * kTokens;
                 if (!(ok = warp_wait(&B.s_full, g & 1u, abort_flag, a.status))) break;
@@ -704,7 +715,7 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                         for (int i = 0; i < 64; ++i) x[i] = -x[i];
                     }
                     if (tail || bad) {
-                        uint2 vis = tail ? visible_bits(bits, walk.n, first, t0) : make_uint2(~0u, ~0u);
+                        uint2 vis = tail ? visible_bits(bits, now.n, first, t0) : make_uint2(~0u, ~0u);
                         if (bad) {
 #pragma unroll
                             for (int k = 0; k < BPI; ++k) {
@@ -737,8 +748,6 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                     // the reference moves only when it would be exceeded by more than 2^8
                     float m_new = m_ref;
                     if (mx * c2 > m_ref + 8.f) m_new = mx * c2;
-                    const float alpha = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
-                    const bool moved = it > walk.it0 && __any_sync(0xffffffffu, alpha != 1.f);
                     const float shift = m_new == -INFINITY ? 0.f : -m_new;  // a row that has seen nothing: P = 0
                     const float2 cc = make_float2(c2, c2), nm = make_float2(shift, shift);
                     float2 ps2a = make_float2(0.f, 0.f), ps2b = make_float2(0.f, 0.f);
@@ -765,6 +774,8 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                         }
                         tmem_st16(t_p + 32 * b + 16 * part, w);
                     }
+                    const float alpha = m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+                    const bool moved = it > it0 && __any_sync(0xffffffffu, alpha != 1.f);
                     l_run = l_run * alpha + ((ps2a.x + ps2b.x) + (ps2a.y + ps2b.y));
                     m_ref = m_new;
                     // rescale O where the reference moved, once O += P(it - 1) V(it - 1) is done
@@ -795,7 +806,7 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                     for (int e = r; e < HALVES * (kTokens - lo) * 8; e += 128) {
                         const int tok = lo + e / (HALVES * 8), hf = e / 8 % HALVES, ch = e % 8;
                         uint4 *at = reinterpret_cast<uint4 *>(vt + hf * Sh::kHalfKV + tok * 128 + ((ch ^ (tok & 7)) << 4));
-                        if (t0 + tok >= walk.L || ((bad >> (tok / BS)) & 1u)) {
+                        if (t0 + tok >= now.L || ((bad >> (tok / BS)) & 1u)) {
                             *at = make_uint4(0u, 0u, 0u, 0u);
                         } else if (t0 + tok >= first) {
                             uint4 v = *at;
@@ -826,16 +837,16 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             if (!ok) break;
             // ---- the piece's end. Of a segment cut in two, whoever gets here first leaves its partial and goes on; the
             // other joins the two from its registers (it waits, if at all, for stores already under way).
-            const bool head = walk.it0 == 0, whole = head && walk.it1 == walk.nit;
+            const bool head = it0 == 0, whole = head && it1 == now.nit;
             int other = -1;  // the CTA of the other piece, where there are two
             if (!whole) {
-                const int end = walk.x + walk.nit - walk.it1;  // the segment's end
+                const int end = now.x + now.nit - it1;  // the segment's end
                 if (head && end <= B.bound_next)
                     other = c + 1;
-                else if (!head && walk.it1 == walk.nit && walk.x - walk.it1 >= B.bound_prev)
+                else if (!head && it1 == now.nit && now.x - it1 >= B.bound_prev)
                     other = c - 1;
                 else if (head && r == 0)
-                    a.cuts[c] = make_int4(walk.q0 + walk.i0, walk.n - walk.i0, walk.h,
+                    a.cuts[c] = make_int4(now.q0 + now.i0, now.n - now.i0, now.h,
                                           static_cast<int>((static_cast<int64_t>(end - B.start) * B.ctas - 1) / B.total) -
                                               B.index + 1);
             }
@@ -878,7 +889,7 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             // a partial is [columns / 4][rows][4]: a warp's rows are side by side
             float4 *own_part = reinterpret_cast<float4 *>(a.o_part + own_row * D) + r;
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                 (static_cast<int64_t>(walk.q0 + draft) * a.num_q_heads + walk.h * G + r % G) * D;
+                                 (static_cast<int64_t>(now.q0 + draft) * a.num_q_heads + now.h * G + r % G) * D;
             if (warp_live) {
 #pragma unroll 1
                 for (int col = 0; col < D; col += 16) {
@@ -923,14 +934,14 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                 }
                 if (poisoned && live) {
                     // the drafts of this piece whose V is not finite, for the rows that see them
-                    const int j1 = min(walk.it1 * kTokens - first, walk.n);
+                    const int j1 = min(it1 * kTokens - first, now.n);
 #pragma unroll 1
-                    for (int j = max(walk.it0 * kTokens - first, 0); j < j1; ++j) {
+                    for (int j = max(it0 * kTokens - first, 0); j < j1; ++j) {
                         if (!((bits[j >> 5] >> (j & 31)) & 1)) continue;
                         const int pos = first + j;
-                        const int p = __ldg(a.block_tables + static_cast<int64_t>(walk.s) * a.max_blocks_per_seq + pos / BS);
+                        const int p = __ldg(a.block_tables + static_cast<int64_t>(now.s) * a.max_blocks_per_seq + pos / BS);
                         if (p < 0 || p >= a.num_blocks) continue;
-                        const int64_t at = ((static_cast<int64_t>(p) * BS + pos % BS) * a.num_kv_heads + walk.h) * D;
+                        const int64_t at = ((static_cast<int64_t>(p) * BS + pos % BS) * a.num_kv_heads + now.h) * D;
 #pragma unroll 1
                         for (int d = 0; d < D; ++d) {
                             float f;
