@@ -25,6 +25,14 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
     return t;
 }
 
+// ---------------------------------------------------------------- dependent launches
+
+// A kernel launched by launch_overlapped may start while the one before it in the stream ends: nothing in global
+// memory is touched before depend_wait(), which returns once that kernel is done and its writes are visible.
+// depend_release() lets the next such kernel start.
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void depend_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count) {

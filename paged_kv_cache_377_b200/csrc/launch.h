@@ -6,9 +6,32 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "decode_common.cuh"
 
 namespace pkv {
+
+// A launch that may overlap the end of the kernel before it (see depend_wait in device_utils.cuh), as a cluster of
+// `cluster` CTAs where that is more than one.
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster,
+                              cudaStream_t stream, Args &&...args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 // kMathFp8: tensor-core (f16 mma.sync) math over e4m3 pools with per-head
 // scales; chosen by the fp8 entry points, not by the math option.

@@ -99,6 +99,8 @@ __global__ void __launch_bounds__(kTableThreads)
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, rank = cluster.block_rank(), ctas = cluster.num_blocks();
     const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+    depend_wait();
+    depend_release();
     const int top = *num_free;
     if (tid == 0) sm.bad = 0;
     __syncthreads();
@@ -202,7 +204,8 @@ __global__ void __launch_bounds__(kSlotThreads)
                         int64_t *slot_mapping, int num_seqs, int num_slots, int max_blocks_per_seq, int block_size,
                         int num_blocks, int32_t *status) {
     extern __shared__ int kept[];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    depend_wait();
+    depend_release();
     const int *starts = query_start;
     if (num_seqs <= kSlotSeqs) {
         for (int s = threadIdx.x; s <= num_seqs; s += kSlotThreads) kept[s] = query_start[s];
@@ -236,6 +239,8 @@ __global__ void __launch_bounds__(kTableThreads)
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, rank = cluster.block_rank(), ctas = cluster.num_blocks();
     const int64_t cap = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+    depend_wait();
+    depend_release();
     const int top = *num_free;
     if (tid == 0) sm.bad = 0;
     __syncthreads();
@@ -307,6 +312,8 @@ __global__ void __launch_bounds__(kMaskThreads)
                      int num_tokens, int max_query_len, int mask_words, int32_t *status) {
     extern __shared__ int2 runs[];  // per node: its run's bits, the node that its run's topmost ancestor hangs from
     const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+    depend_wait();
+    depend_release();
     const int q0 = query_start[s], q1 = query_start[s + 1], n = q1 - q0;
     if (q0 < 0 || n < 0 || q1 > num_tokens || n > max_query_len) {
         if (tid == 0) atomicOr(status, PKV_STATUS_BAD_CONTEXT_LEN);
@@ -368,6 +375,8 @@ __global__ void __launch_bounds__(kKeepThreads)
     const int c = blockIdx.z * kKeepThreads + tid;
     uint4 *pool = blockIdx.y ? v_cache : k_cache;
     const bool first = blockIdx.y == 0 && blockIdx.z == 0;
+    depend_wait();
+    depend_release();
     const int L = context_lens[s], n = query_start[s + 1] - query_start[s], a = num_accepted[s];
     const int32_t *path = accepted + static_cast<int64_t>(s) * max_accepted;
     const int32_t *table = block_tables + static_cast<int64_t>(s) * max_blocks_per_seq;
@@ -429,20 +438,6 @@ int table_ctas(int64_t items) {
     return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : 8;
 }
 
-cudaLaunchConfig_t table_config(int ctas, cudaLaunchAttribute *attr, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kTableThreads);
-    cfg.stream = stream;
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = ctas;
-    attr->val.clusterDim.y = 1;
-    attr->val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 1 : 0;  // a launch without the attribute is a cluster of one, and sooner made
-    return cfg;
-}
-
 // Steps of more slots than this leave them to tables_slots_kernel.
 constexpr int kClusterSlots = 16384;
 
@@ -453,43 +448,36 @@ cudaError_t tables_grow_launch(int32_t *block_tables, const int32_t *context_len
                                int32_t *query_start, int64_t *slot_mapping, int32_t *num_free_out, int num_seqs,
                                int num_slots, int max_blocks_per_seq, int block_size, int num_blocks, int32_t *status,
                                cudaStream_t stream) {
-    cudaLaunchAttribute attr;
     const bool few = num_slots <= kClusterSlots;
-    cudaLaunchConfig_t cfg = table_config(table_ctas(few ? num_slots : num_slots / block_size + num_seqs), &attr, stream);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, few ? tables_grow_kernel<true> : tables_grow_kernel<false>, block_tables,
-                                       context_lens, new_tokens, free_blocks, num_free, new_lens, query_start,
-                                       slot_mapping, num_free_out, num_seqs, num_slots, max_blocks_per_seq, block_size,
-                                       num_blocks, status);
+    const int ctas = table_ctas(few ? num_slots : num_slots / block_size + num_seqs);
+    cudaError_t e = launch_overlapped(few ? tables_grow_kernel<true> : tables_grow_kernel<false>, dim3(ctas),
+                                      kTableThreads, 0, ctas, stream, block_tables, context_lens, new_tokens,
+                                      free_blocks, num_free, new_lens, query_start, slot_mapping, num_free_out, num_seqs,
+                                      num_slots, max_blocks_per_seq, block_size, num_blocks, status);
     if (e != cudaSuccess || few) return e;
     const int blocks = (num_slots + kSlotThreads - 1) / kSlotThreads;
-    cfg.gridDim = dim3(blocks < 148 * 8 ? blocks : 148 * 8);
-    cfg.blockDim = dim3(kSlotThreads);
-    cfg.dynamicSmemBytes = num_seqs <= kSlotSeqs ? (static_cast<size_t>(num_seqs) + 1) * 4 : 0;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tables_slots_kernel, static_cast<const int32_t *>(block_tables),
-                              static_cast<const int32_t *>(new_lens), static_cast<const int32_t *>(query_start),
-                              slot_mapping, num_seqs, num_slots, max_blocks_per_seq, block_size, num_blocks, status);
+    return launch_overlapped(tables_slots_kernel, dim3(blocks < 148 * 8 ? blocks : 148 * 8), kSlotThreads,
+                             num_seqs <= kSlotSeqs ? (static_cast<size_t>(num_seqs) + 1) * 4 : 0, 1, stream,
+                             block_tables, new_lens, query_start, slot_mapping, num_seqs, num_slots, max_blocks_per_seq,
+                             block_size, num_blocks, status);
 }
 
 cudaError_t tables_trim_launch(const int32_t *block_tables, const int32_t *context_lens, const int32_t *keep_lens,
                                int32_t *free_blocks, const int32_t *num_free, int32_t *num_free_out, int num_seqs,
                                int max_blocks_per_seq, int block_size, int num_blocks, int32_t *status,
                                cudaStream_t stream) {
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg =
-        table_config(table_ctas(static_cast<int64_t>(num_seqs) * max_blocks_per_seq), &attr, stream);
-    return cudaLaunchKernelEx(&cfg, tables_trim_kernel, block_tables, context_lens, keep_lens, free_blocks, num_free,
-                              num_free_out, num_seqs, max_blocks_per_seq, block_size, num_blocks, status);
+    const int ctas = table_ctas(static_cast<int64_t>(num_seqs) * max_blocks_per_seq);
+    return launch_overlapped(tables_trim_kernel, dim3(ctas), kTableThreads, 0, ctas, stream, block_tables, context_lens,
+                             keep_lens, free_blocks, num_free, num_free_out, num_seqs, max_blocks_per_seq, block_size,
+                             num_blocks, status);
 }
 
 cudaError_t tree_mask_launch(int32_t *tree_mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
                              int num_seqs, int num_tokens, int max_query_len, int mask_words, int32_t *status,
                              cudaStream_t stream) {
-    tree_mask_kernel<<<num_seqs, kMaskThreads, static_cast<size_t>(max_query_len) * 8, stream>>>(
-        tree_mask, depths, parents, query_start, num_tokens, max_query_len, mask_words, status);
-    return cudaGetLastError();
+    return launch_overlapped(tree_mask_kernel, dim3(num_seqs), kMaskThreads, static_cast<size_t>(max_query_len) * 8, 1,
+                             stream, tree_mask, depths, parents, query_start, num_tokens, max_query_len, mask_words,
+                             status);
 }
 
 cudaError_t cache_keep_launch(void *k_cache, void *v_cache, const int32_t *block_tables, const int32_t *context_lens,
@@ -498,10 +486,10 @@ cudaError_t cache_keep_launch(void *k_cache, void *v_cache, const int32_t *block
                               int max_blocks_per_seq, int num_blocks, int32_t *status, cudaStream_t stream) {
     const int chunks = row_bytes / 16;
     const dim3 grid(num_seqs, 2, (chunks + kKeepThreads - 1) / kKeepThreads);
-    cache_keep_kernel<<<grid, kKeepThreads, 0, stream>>>(
-        static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), block_tables, context_lens, query_start,
-        accepted, num_accepted, new_lens, max_accepted, chunks, block_size, max_blocks_per_seq, num_blocks, status);
-    return cudaGetLastError();
+    return launch_overlapped(cache_keep_kernel, grid, kKeepThreads, 0, 1, stream, static_cast<uint4 *>(k_cache),
+                             static_cast<uint4 *>(v_cache), block_tables, context_lens, query_start, accepted,
+                             num_accepted, new_lens, max_accepted, chunks, block_size, max_blocks_per_seq, num_blocks,
+                             status);
 }
 
 }  // namespace pkv

@@ -327,6 +327,8 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
         tma_prefetch_desc(&tm_v);
     }
 
+    depend_wait();
+    depend_release();
     // ---- weights: every CTA sums over all sequences (one contiguous run per thread)
     const int entries = a.num_seqs * a.lists;
     {
@@ -989,7 +991,8 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeArg
     __shared__ float2 ml_s[kMergeWarps][32];
     __shared__ float4 o_s[kMergeWarps][kMergeQuads][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    depend_wait();
+    depend_release();
     for (int k = warp; k < kTreeMaxCtas / 32; k += kMergeWarps) {
         const int c = k * 32 + lane;
         const unsigned m = __ballot_sync(0xffffffffu, c < ctas && a.cuts[c].w != 0);
@@ -1104,20 +1107,12 @@ cudaError_t launch(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUten
         if (e != cudaSuccess) return e;
         prepared |= bit;
     }
-    fn<<<ctas, TreeShape<D, FP8>::kThreads, smem, stream>>>(tm_q, tm_k, tm_v, a);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.whole || ctas == 1) return e;
+    e = launch_overlapped(fn, dim3(ctas), TreeShape<D, FP8>::kThreads, smem, 1, stream, tm_q, tm_k, tm_v, a);
+    if (e != cudaSuccess || a.whole || ctas == 1) return e;
     const int rows = (a.max_query_len < a.tile_drafts ? a.max_query_len : a.tile_drafts) * a.group;
-    cudaLaunchConfig_t cfg{};
     const int row_chunks = (rows + 31) / 32, most = ctas / 2 * row_chunks * (D / kMergeCols);  // three pieces or more each
-    cfg.gridDim = dim3(most < kMergeCtas ? (most > 0 ? most : 1) : kMergeCtas);
-    cfg.blockDim = dim3(kMergeThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, a, ctas, row_chunks);
+    return launch_overlapped(tree_merge_kernel<D>, dim3(most < kMergeCtas ? most : kMergeCtas), kMergeThreads, 0, 1,
+                             stream, a, ctas, row_chunks);
 }
 
 template <bool FP8>
