@@ -451,15 +451,26 @@ int kv_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
  *               = draft j of the same sequence is seen; bits past n_s are
  *               ignored; mask_words * 32 >= max_query_len
  * max_query_len host int: the largest n_s, at most PKV_MAX_TREE_TOKENS
- * workspace     device, pkv_tree_workspace_bytes() bytes, 256-byte aligned; its
- *               first int32 is the status word, ORed and never cleared by this
- *               call. Calls that may overlap need one each.
+ * workspace     device, pkv_tree_workspace_bytes() bytes, 256-byte aligned, zeroed
+ *               once before its first use and left alone since; its first int32
+ *               is the status word, ORed and never cleared by this call. One
+ *               serves calls of any shape one after another (a stream, a graph,
+ *               several graphs in turn); calls that may overlap need one each.
  * A sequence whose query_start or context length is inconsistent is skipped
  * (its rows are left as they were) and sets PKV_STATUS_BAD_CONTEXT_LEN; a bad
  * table entry sets PKV_STATUS_BAD_BLOCK_ID and its positions are not seen.
- * Supported: as paged_attn_decode, with any number of sequences.
+ * Supported: as paged_attn_decode (head_dim 64 / 128, block_size 16 / 32, group
+ * <= 8), with any number of sequences and block tables of any width. bf16
+ * products and fp32 sums on tcgen05, probabilities rounded to bf16. For a given
+ * device and batch shape, results are bitwise reproducible and do not depend on
+ * where blocks sit in the pool. Per call (and per 1024 sequences): one kernel,
+ * and one that joins contexts cut in more than two, unless the tables are too
+ * short for a cut (512 tokens).
  *
- * paged_attn_tree_fp8: the same over e4m3 pools with per-kv-head scales.
+ * paged_attn_tree_fp8: the same over e4m3 pools with per-kv-head scales (and per
+ * 512 sequences). Q is scaled per row by a power of two and split into two e4m3
+ * terms (eight bits); K's codes are multiplied as they are, V's widened to f16,
+ * exactly, and probabilities rounded to f16.
  */
 #define PKV_MAX_TREE_TOKENS 4096
 int pkv_tree_workspace_bytes(int head_dim, size_t *bytes);

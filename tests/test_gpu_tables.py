@@ -124,6 +124,56 @@ def test_grow_is_all_or_nothing(why, bit):
     assert torch.equal(tables, b.block_tables) and torch.equal(stack, b.free_blocks)
 
 
+@pytest.mark.parametrize("why,bit", [("blocks", 64), ("negative", 2)])
+def test_large_steps_are_all_or_nothing_too(why, bit):
+    """More slots than one cluster takes: the second kernel writes nothing but -1."""
+    lens, add = np.full(500, 21), np.full(500, 60)
+    b = Tables(31, lens, 16, 6, 500 * 2 + (500 * 4 - 1 if why == "blocks" else 3000))
+    if why == "negative":
+        add[77] = -5
+    tables, before, free = b.block_tables.clone(), b.context_lens.tolist(), int(b.num_free)
+    assert b.grow(add, 30001) == (before, [0] * 501, [-1] * 30001, free)
+    assert pkv.read_status(b.status) == bit and torch.equal(tables, b.block_tables)
+
+
+def test_bad_ids_of_a_large_step_are_flagged():
+    b = Tables(32, [5, 16], 16, 2000, 4100)
+    b.free_blocks[int(b.num_free) - 2] = 5000      # the second block taken
+    got = b.grow([20000, 30], 20040)
+    assert pkv.read_status(b.status) == pkv.PKV_STATUS_BAD_BLOCK_ID
+    bad = [i for i, s in enumerate(got[2][:20030]) if s < 0]
+    assert bad == list(range(27, 43)) and got[2][20030:] == [-1] * 10
+
+
+def test_grow_and_trim_back_to_back_without_a_wait():
+    """A hundred steps that lean on one another, each started while the one before ends."""
+    rng = np.random.default_rng(33)
+    lens = rng.integers(0, 50, size=300)
+    b = Tables(33, lens, 16, 20, 5000)
+    S = 300
+    qs = torch.zeros(S + 1, dtype=torch.int32, device=DEV)
+    slots = torch.zeros(20000, dtype=torch.int64, device=DEV)
+    adds = [rng.integers(0, 9, size=S) for _ in range(50)]
+    keeps, L = [], lens.copy()
+    for a in adds:
+        L = L + a
+        keeps.append(np.maximum(L - rng.integers(0, 7, size=S), 0))
+        L = keeps[-1]
+    dadds, dkeeps = [dev(a) for a in adds], [dev(k) for k in keeps]
+    for a, k in zip(dadds, dkeeps):
+        pkv.kv_tables_grow(b.block_tables, b.context_lens, a, b.free_blocks, b.num_free, b.context_lens, qs, slots,
+                           b.num_free, 16, b.status)
+        pkv.kv_tables_trim(b.block_tables, b.context_lens, k, b.free_blocks, b.num_free, b.num_free, 16, b.status)
+        b.context_lens.copy_(k)
+    torch.cuda.synchronize()
+    for a, k in zip(adds, keeps):
+        want = b.plain_grow(a)
+        b.plain_trim(k)
+    assert slots.tolist()[:len(want[1])] == want[1] and qs.tolist() == want[0]
+    b.assert_same()
+    assert pkv.read_status(b.status) == 0
+
+
 def test_bad_ids_and_counts_are_flagged():
     b = Tables(4, [5, 16], 16, 4, 10)
     b.free_blocks[int(b.num_free) - 1] = 99

@@ -79,6 +79,35 @@ def test_long_contexts_of_few_sequences(seqs, base, nodes, heads, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_trees_of_many_tiles(fp8):
+    """600 and 257 drafts of eight heads a group: dozens of row tiles in pairs, odd ones out, beside one-draft trees."""
+    check(make_step(43, [90, 3, 700, 0], [600, 1, 257, 16], 8, 1, 64, 16, fp8=fp8), "many tiles")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_and_two_tile_trees_together(fp8):
+    """Contexts that are cut, some with a pair of row tiles, some with one: three groups of CTAs."""
+    check(make_step(45, [3000, 2500, 10, 1800, 0], [26, 5, 19, 18, 36], 14, 2, 128, 32, fp8=fp8), "mixed tiles")
+
+
+def test_one_workspace_serves_calls_of_every_kind_in_turn():
+    """Batches of other shapes, head sizes and pools follow one another through one workspace, without a wait."""
+    ws = pkv.allocate_tree_workspace(128, device=DEV)
+    steps = [make_step(81, [5000, 40], [16, 3], 8, 2, 128, 16), make_step(82, [3000], [40], 4, 1, 64, 32, fp8=True),
+             make_step(83, [20, 9, 0], [3, 5, 1], 4, 2, 64, 16), make_step(84, [900] * 5, [20] * 5, 14, 2, 128, 16, fp8=True),
+             make_step(85, [2400, 2000], [70, 12], 8, 2, 128, 32)]
+    runs = [(s, torch.full(s.q.shape, SENTINEL, dtype=torch.bfloat16, device=DEV), device_args(s)) for s in steps]
+    for _ in range(3):
+        for s, out, args in runs:
+            call(s, out, args, ws)
+    torch.cuda.synchronize()
+    assert pkv.read_status(ws) == 0
+    for s, out, _ in runs:
+        ref, spread = attention(s)
+        assert_close(out.double().cpu().numpy(), ref, spread, s.fp8, "in turn")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_skewed_batch(fp8):
     rng = np.random.default_rng(3)
     base = np.concatenate([[6000, 1500], rng.integers(0, 100, size=30)])
