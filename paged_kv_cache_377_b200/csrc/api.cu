@@ -853,6 +853,9 @@ int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const voi
     // 12; over e4m3 pools, where a piece's queries are split too, 139 at 2, 120 at 6 to 8)
     a.piece_cost = fp8 ? 7 : 4;
     const int64_t most_it = (static_cast<int64_t>(max_blocks_per_seq) * block_size + 63) / 64;
+    // Tables too short for a cut to pay (512 tokens): whole segments, and no second kernel (64 sequences of 125 .. 250
+    // tokens: 24.5 us whole, 28.7 cut; one of 900: 16.1 and 13.0). Otherwise a CTA for every four iterations (one
+    // sequence of 900 tokens: 13.0 us; one for every eight: 19.2).
     a.whole = most_it <= 8;
     a.min_weight = a.whole ? 1 : 4;
     // A launch's weights are 32-bit sums: at most so many sequences as cannot pass them.
