@@ -135,8 +135,9 @@ struct TreeShape {
 
 // A warp's `span` rows of codes (dense, D bytes each) into rows tok0 .. of an operand tile ([64-column half][row][128
 // bytes], swizzled), as f16 (exact). Eight rows of four 16-code chunks a step; rows and halves alternate so that neither
-// side's banks meet; four steps' codes are loaded before the first is stored (one by one, a step waited 280 cycles).
-// The hardware's conversion takes two codes in 2 cycles a warp; placing their bits by hand took 8.
+// side's banks meet; four steps' codes are loaded before the first is stored, so that their latencies overlap.
+// The hardware's conversion takes two codes in 2.0 cycles a warp; placing their bits by hand takes several integer
+// instructions of 2.2 to 2.8 each.
 template <int D>
 __device__ __forceinline__ void widen_rows(const uint8_t *src, uint8_t *dst, int tok0, int span, int lane) {
     constexpr int HALVES = D / 64, BATCH = 4;
@@ -170,7 +171,7 @@ __device__ __forceinline__ void widen_rows(const uint8_t *src, uint8_t *dst, int
 // + q2 with f a power of two that puts the row's largest magnitude in [2^7, 2^8). q1 keeps four bits, q2 the next four
 // (what is below 2^-10 of q f is lost: 2^-17 of the row's largest). Eight lanes a row, four rows a step. Returns 1 / f of
 // the lane's own row (NaN for a row that is not finite: its logits all are). A loop, like all that runs once a piece:
-// unrolled, it took 10,000 cycles to fetch.
+// unrolled, it took 6,000 to 10,000 cycles a piece.
 template <int D>
 __device__ __forceinline__ float split_queries(uint8_t *sq, int row0, int lane) {
     constexpr int HALVES = D / 64;
@@ -864,7 +865,7 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             const int64_t other_row = (other * 2 + (head ? 0 : 1)) * static_cast<int64_t>(kRows);
             const float4 *other_part = reinterpret_cast<const float4 *>(a.o_part + other_row * D) + r;
             float scale_mine = l_run == 0.f ? 0.f : 1.f / l_run, scale_other = 0.f;
-            float4 v[4];  // the other piece's next 16 columns, asked for ahead (one by one, they took 12,000 cycles)
+            float4 v[4];  // the other piece's next 16 columns, asked for ahead: one by one, they wait in turn
             if (join) {
                 if (!(ok = wait_stored(count, abort_flag, a.status))) break;
                 const float2 ml = a.ml_part[other_row + r];
