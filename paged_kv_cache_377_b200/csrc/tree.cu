@@ -47,6 +47,11 @@ namespace {
 constexpr int kRows = 128;       // rows of a tile (= tensor-memory lanes)
 constexpr int kTokens = 64;      // positions of one iteration
 constexpr int kBadRing = 8;      // iterations whose bad-block bits are kept (a loader is at most 5 ahead)
+// Copies of what the softmax warps tell one another once a piece, by the piece's parity. One would not do: a warp may
+// read a piece's word as late as the end of its stores, and nothing holds the others back until it loads S of the next
+// piece's first iteration; if that is also its last one, they write the next piece's word before. Past that iteration
+// they wait for it, so that the word of the piece after next is safe.
+constexpr int kPieceSlots = 2;
 
 // A CTA's share of the step, piece by piece (a piece: consecutive iterations of
 // one segment). Every role walks it alike.
@@ -240,8 +245,8 @@ struct TreeBars {
     uint32_t bad[kBadRing];  // blocks without a place in the pool, a bit each
     uint32_t tmem;
     int abort;
-    int arrived;
-    int poison[2];
+    int arrived[kPieceSlots];
+    int poison[kPieceSlots];
     Walk walk[4];  // the softmax warps' pieces
     int start, total, ctas, index;  // the CTA's group: weight positions, CTAs, and its own place among them
     int bound_prev, bound_next;     // where the share of the CTA before begins and of the CTA after ends
@@ -319,8 +324,8 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&B.p_ready[i], kSoftmaxWarps);
             mbar_init(&B.pv_free[i], 1);
-            B.poison[i] = 0;
         }
+        for (int i = 0; i < kPieceSlots; ++i) B.poison[i] = 0;
         B.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -681,7 +686,7 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             if (lane == 0) now = next;
             __syncwarp();
             if (!more) break;
-            const uint32_t piece = pieces++;
+            const uint32_t piece = pieces++, slot = piece % kPieceSlots;
             const int it0 = next.it0, it1 = next.it1, first = next.L - next.n;  // first draft's position
             const int draft = next.i0 + r / G;
             const bool live = !spare && draft < next.n;
@@ -827,7 +832,7 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                                 }
                             }
                             if (any) {
-                                poison[piece & 1u] = 1;
+                                poison[slot] = 1;
                                 *at = v;
                             }
                         }
@@ -854,11 +859,11 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                                               B.index + 1);
             }
             unsigned *count = a.arrivals + (head ? c : c - 1);
-            if (other >= 0 && r == 0) B.arrived = static_cast<int>(atomicAdd(count, 1u) & 15u);
+            if (other >= 0 && r == 0) B.arrived[slot] = static_cast<int>(atomicAdd(count, 1u) & 15u);
             bool join = false;
             if (other >= 0) {
                 if (!meet_all()) break;  // all know which comes first
-                join = *reinterpret_cast<volatile int *>(&B.arrived) != 0;
+                join = *reinterpret_cast<volatile int *>(&B.arrived[slot]) != 0;
             }
             const bool store = !whole && !join;
             const int64_t own_row = (c * 2 + (head ? 1 : 0)) * static_cast<int64_t>(kRows);
@@ -884,10 +889,10 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
             }
             if (!(ok = warp_wait(&B.o_full, piece & 1u, abort_flag, a.status))) break;
             tc_fence_after();
-            const bool poisoned = poison[piece & 1u] != 0;
+            const bool poisoned = poison[slot] != 0;
             if (poisoned) {
                 if (!meet_all()) break;  // all have read the flag
-                if (r == 0) poison[piece & 1u] = 0;
+                if (r == 0) poison[slot] = 0;
             }
             // a partial is [columns / 4][rows][4]: a warp's rows are side by side
             float4 *own_part = reinterpret_cast<float4 *>(a.o_part + own_row * D) + r;
