@@ -30,8 +30,10 @@
 // of two, is split into two e4m3 terms (four bits each of its eight), and S = Q1 K^T
 // + Q2 K^T on kind::f8f6f4 costs what one bf16 product does. V is widened to f16 by
 // two warps, exactly, and P written in f16: e4m3 terms of P would lose the small
-// weights of a long context beside a large one. (Widening K to bf16 as well kept the
-// integer pipe busy for longer than the copies take.)
+// weights of a long context beside a large one. f16 has its own floor, so P's largest
+// is kept between 2^7 and 2^15: weights down to 2^-21 of it keep eleven bits, the next
+// ones steps of 2^-24 in P, and what is below 2^-32 of it rounds to zero. (Widening K to
+// bf16 as well kept the integer pipe busy for longer than the copies take.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -665,6 +667,10 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
         bool negative = a.scale_log2 < 0.f;
         const bool spare = r >= a.tile_drafts * G;
         volatile int *poison = B.poison;
+        // How far below a maximum the reference is put: with the 2^8 that it may lag behind, f16 (to 65504) has room for
+        // 2^7. O, the sum and the partials belong to the reference as it is, so that it cancels. (8192 weights about
+        // 2^-24.5 of a large one, P alone rounded: their sum is off by up to 7 % without, by 0.02 % with it.)
+        constexpr float kLift = FP8 ? 7.f : 0.f;
         uint32_t g = 0, pieces = 0, met_all = 0;
         bool ok = true;
         auto signal = [&](uint64_t *bar) {  // one arrival per warp, after all its lanes
@@ -753,9 +759,9 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                         for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[60 + e]);
                         mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
                     }
-                    // the reference moves only when it would be exceeded by more than 2^8
+                    // the reference, kLift below a maximum, moves only when that would be exceeded by more than 2^8
                     float m_new = m_ref;
-                    if (mx * c2 > m_ref + 8.f) m_new = mx * c2;
+                    if (mx * c2 > m_ref + (kLift + 8.f)) m_new = mx * c2 - kLift;
                     const float shift = m_new == -INFINITY ? 0.f : -m_new;  // a row that has seen nothing: P = 0
                     const float2 cc = make_float2(c2, c2), nm = make_float2(shift, shift);
                     float2 ps2a = make_float2(0.f, 0.f), ps2b = make_float2(0.f, 0.f);

@@ -1,0 +1,50 @@
+"""paged_attn_tree over rows that real heads have and random ones do not: one large weight beside thousands of small
+ones."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_tree import check
+from tree_reference import make_step
+
+pytestmark = pytest.mark.gpu
+
+
+def sink_step(fp8, gap, at, L=8192, seqs=20, heads=16):
+    """``seqs`` sequences of one draft each over the same L tokens: so many that a CTA walks about a whole context.
+    Token ``at`` has a logit ``gap`` above the middle of the others', whose logits are N(0, 0.75) or so, and V = 0;
+    the others' V are positive."""
+    step = make_step(95, [L - 1], [1], heads, heads, 64, 16, fp8=fp8)
+    p, off = int(step.block_tables[0, at // 16]), at % 16
+    if fp8:
+        step.k_scale[:] = 2.0 ** -4
+        step.v_scale[:] = 2.0 ** -4
+        step.v_cache &= 0x7F
+        step.k_cache[..., 0] = 0
+        step.k_cache[p, off] = 0
+        step.k_cache[p, off, :, 0] = 0x78            # 256, which the scale makes 16
+        step.v_cache[p, off] = 0
+    else:
+        step.v_cache = step.v_cache.abs()
+        step.k_cache[..., 0] = 0
+        step.k_cache[p, off] = 0
+        step.k_cache[p, off, :, 0] = 16
+        step.v_cache[p, off] = 0
+    step.q = torch.randn(seqs, heads, 64, generator=torch.Generator().manual_seed(96)).to(torch.bfloat16)
+    step.q[..., 0] = gap / 2                         # times 16 times the scale of 1/8
+    step.block_tables = step.block_tables.repeat(seqs, 1)
+    step.context_lens = step.context_lens.repeat(seqs)
+    step.query_start = torch.arange(seqs + 1, dtype=torch.int32)
+    step.tree_mask = torch.ones(seqs, 1, dtype=torch.int32)
+    step.sees = [np.ones((1, 1), dtype=bool)] * seqs
+    return step
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("at", [0, 6000])
+@pytest.mark.parametrize("gap", [11, 13, 15, 17])
+def test_small_weights_beside_a_large_one_add_up(gap, at, fp8):
+    """What the sums' rounding to f16 may do to a weight e^-17 of the largest, 2^-24.5 of it: kept 2^7 higher it is
+    2^-17.5, a step of f16 there 2^-24, so one weight is off by up to 2^-7.5 of itself and eight thousand of unlike
+    ones together by 2^-7.5 / sqrt(3 x 8192), less than a tenth of the 2^-11 that is granted."""
+    check(sink_step(fp8, gap, at), f"a weight {gap} nats above the others")
