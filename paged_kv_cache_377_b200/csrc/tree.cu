@@ -177,7 +177,8 @@ __device__ __forceinline__ void widen_rows(const uint8_t *src, uint8_t *dst, int
 // A warp's 32 rows of the query tile, in place: the 64 bf16 of each 128-byte slab row become 64 + 64 e4m3 codes, q f = q1
 // + q2 with f a power of two that puts the row's largest magnitude in [2^7, 2^8). q1 keeps four bits, q2 the next four
 // (what is below 2^-10 of q f is lost: 2^-17 of the row's largest). Eight lanes a row, four rows a step. Returns 1 / f of
-// the lane's own row (NaN for a row that is not finite: its logits all are). A loop, like all that runs once a piece:
+// the lane's own row. A row that is not finite becomes codes of NaN, as all its logits are: what it does not see is
+// hidden behind them like any other, so the factor stays finite. A loop, like all that runs once a piece:
 // unrolled, it took 6,000 to 10,000 cycles a piece.
 template <int D>
 __device__ __forceinline__ float split_queries(uint8_t *sq, int row0, int lane) {
@@ -205,7 +206,7 @@ __device__ __forceinline__ float split_queries(uint8_t *sq, int row0, int lane) 
         for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         const int e = static_cast<int>(top >> 7);                                                  // exponent field
         const float f = __uint_as_float(static_cast<uint32_t>(min(261 - e, 247)) << 23);           // 2^(134 - e) or 2^120
-        const float inv = e == 255 ? NAN : __uint_as_float(static_cast<uint32_t>(max(e - 7, 7)) << 23);
+        const float inv = __uint_as_float(static_cast<uint32_t>(max(e - 7, 7)) << 23);
         const float its = __shfl_sync(0xffffffffu, inv, (lane & 3) * 8);
         if ((lane >> 2) == step) mine = its;
 #pragma unroll
@@ -223,6 +224,7 @@ __device__ __forceinline__ float split_queries(uint8_t *sq, int row0, int lane) 
                 w1[i >> 1] |= static_cast<uint32_t>(c1) << (16 * (i & 1));
                 w2[i >> 1] |= static_cast<uint32_t>(c2) << (16 * (i & 1));
             }
+            if (e == 255) w1[0] = w1[1] = w2[0] = w2[1] = 0x7f7f7f7fu;
             __syncwarp();  // the rows' slabs are read
             uint8_t *slab = row + hf * (kRows * 128) + (ch & 1) * 8;
             *reinterpret_cast<uint2 *>(slab + (((ch >> 1) ^ (r & 7)) << 4)) = make_uint2(w1[0], w1[1]);

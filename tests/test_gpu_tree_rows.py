@@ -1,11 +1,11 @@
 """paged_attn_tree over rows that real heads have and random ones do not: one large weight beside thousands of small
-ones."""
+ones, and queries that are not finite."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_tree import check
-from tree_reference import make_step
+from test_gpu_tree import check, run
+from tree_reference import assert_close, attention, make_step
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,24 @@ def test_small_weights_beside_a_large_one_add_up(gap, at, fp8):
     2^-17.5, a step of f16 there 2^-24, so one weight is off by up to 2^-7.5 of itself and eight thousand of unlike
     ones together by 2^-7.5 / sqrt(3 x 8192), less than a tenth of the 2^-11 that is granted."""
     check(sink_step(fp8, gap, at), f"a weight {gap} nats above the others")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_not_finite_stays_in_its_row(value, fp8):
+    """Zeros where the row sees nothing, NaN where it sees something (its logits are infinite or NaN), and the other
+    rows as they were."""
+    step = make_step(97, [0, 50, 0], [40, 8, 3], 8, 2, 128, 16, fp8=fp8, kind="any")
+    ref, spread = attention(step)
+    blind = [i for i in range(40) if not step.sees[0][i].any()]
+    seeing = [i for i in range(40) if step.sees[0][i].sum() > 8]
+    assert len(blind) > 2 and len(seeing) > 2
+    hit = np.zeros(51, dtype=bool)
+    for i in (blind[0], blind[2], seeing[0], seeing[2], 43):
+        step.q[i, :, 5] = value
+        hit[i] = True
+    out, st = run(step)
+    assert st == 0
+    assert (out[[blind[0], blind[2]]] == 0).all()
+    assert np.isnan(out[[seeing[0], seeing[2], 43]]).all()
+    assert_close(out[~hit], ref[~hit], spread[~hit], fp8, "the rows beside")
