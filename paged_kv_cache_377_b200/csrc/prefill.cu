@@ -27,6 +27,7 @@
 
 #include "device_utils.cuh"
 #include "launch.h"
+#include "step_utils.cuh"
 #include "mma_utils.cuh"
 
 namespace pkv {
@@ -58,11 +59,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     // ---- the sequence: its chunk of queries and its causal extent (uniform per CTA)
-    const int q0 = __ldg(a.query_start + s), q1 = __ldg(a.query_start + s + 1);
-    const int n = q1 - q0;
+    int q0, n;
+    const bool rows_good = query_rows(a.query_start, s, a.num_tokens, q0, n);
     const int L = __ldg(a.context_lens + s);
-    if (n < 0 || q0 < 0 || q1 > a.num_tokens || n > L || L > a.max_blocks_per_seq * BS ||
-        n > a.max_query_len) {
+    if (!rows_good || n > L || L > a.max_blocks_per_seq * BS || n > a.max_query_len) {
         if (tile == 0 && h == 0 && tid == 0) atomicOr(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
         return;
     }

@@ -10,6 +10,7 @@
 
 #include "device_utils.cuh"
 #include "launch.h"
+#include "step_utils.cuh"
 
 namespace pkv {
 namespace {
@@ -336,8 +337,8 @@ __global__ void __launch_bounds__(kMaskThreads)
     const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     depend_wait();
     depend_release();
-    const int q0 = query_start[s], q1 = query_start[s + 1], n = q1 - q0;
-    if (q0 < 0 || n < 0 || q1 > num_tokens || n > max_query_len) {
+    int q0, n;
+    if (!query_rows(query_start, s, num_tokens, q0, n) || n > max_query_len) {
         if (tid == 0) atomicOr(status, PKV_STATUS_BAD_CONTEXT_LEN);
         return;
     }
@@ -399,12 +400,14 @@ __global__ void __launch_bounds__(kKeepThreads)
     const bool first = blockIdx.y == 0 && blockIdx.z == 0;
     depend_wait();
     depend_release();
-    const int L = context_lens[s], n = query_start[s + 1] - query_start[s], a = num_accepted[s];
+    int q0, n;
+    const bool rows_good = query_rows(query_start, s, 0x7fffffff, q0, n);  // (the step's rows are not read here)
+    const int L = context_lens[s], a = num_accepted[s];
     const int32_t *path = accepted + static_cast<int64_t>(s) * max_accepted;
     const int32_t *table = block_tables + static_cast<int64_t>(s) * max_blocks_per_seq;
     if (tid == 0) bad = 0;
     __syncthreads();
-    if (L < 0 || n < 0 || n > L || L > static_cast<int64_t>(max_blocks_per_seq) * block_size) {
+    if (!rows_good || L < 0 || n > L || L > static_cast<int64_t>(max_blocks_per_seq) * block_size) {
         if (tid == 0) bad = PKV_STATUS_BAD_CONTEXT_LEN;
     } else if (a < 0 || a > n || a > max_accepted) {
         if (tid == 0) bad = PKV_STATUS_BAD_TREE;

@@ -41,6 +41,7 @@
 
 #include "device_utils.cuh"
 #include "launch.h"
+#include "step_utils.cuh"
 #include "tcgen05_utils.cuh"
 
 namespace pkv {
@@ -346,11 +347,10 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
         const int s0 = min(tid * per, a.num_seqs), s1 = min(s0 + per, a.num_seqs);
         int sum[2] = {0, 0};
         for (int s = s0; s < s1; ++s) {
-            const int q0 = __ldg(a.query_start + s), n = __ldg(a.query_start + s + 1) - q0;
+            int q0, n, tiles = 0;
+            const bool rows_good = query_rows(a.query_start, s, a.num_tokens, q0, n);
             const int L = __ldg(a.context_lens + s);
-            int tiles = 0;
-            if (q0 < 0 || n < 0 || q0 > a.num_tokens - n || n > a.max_query_len || n > L ||
-                L > static_cast<int64_t>(a.max_blocks_per_seq) * BS) {
+            if (!rows_good || n > a.max_query_len || n > L || L > static_cast<int64_t>(a.max_blocks_per_seq) * BS) {
                 if (blockIdx.x == 0) atomicOr(a.status, PKV_STATUS_BAD_CONTEXT_LEN);
             } else {
                 tiles = (n + a.tile_drafts - 1) / a.tile_drafts;
