@@ -141,7 +141,7 @@ def decode_sources_sha():
 def prefill_sources_sha():
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "paged_kv_cache_377_b200", "csrc")
-    for name in ("prefill_tc.cu", "device_utils.cuh"):
+    for name in ("prefill_tc.cu", "tcgen05_utils.cuh", "step_utils.cuh", "device_utils.cuh"):
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]

@@ -12,7 +12,7 @@
 
 namespace pkv {
 
-// A launch that may overlap the end of the kernel before it (see depend_wait in device_utils.cuh), as a cluster of
+// A launch that may overlap the end of the kernel before it (see depend_wait in step_utils.cuh), as a cluster of
 // `cluster` CTAs where that is more than one.
 template <typename... Params, typename... Args>
 cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster,
