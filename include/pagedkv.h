@@ -460,7 +460,7 @@ int kv_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
  * (its rows are left as they were) and sets PKV_STATUS_BAD_CONTEXT_LEN; a bad
  * table entry sets PKV_STATUS_BAD_BLOCK_ID and its positions are not seen.
  * Supported: as paged_attn_decode (head_dim 64 / 128, block_size 16 / 32, group
- * <= 8), with any number of sequences and block tables of any width. bf16
+ * <= 8), with any number of sequences and block tables of up to 2^31 - 64 tokens. bf16
  * products and fp32 sums on tcgen05, probabilities rounded to bf16. For a given
  * device and batch shape, results are bitwise reproducible and do not depend on
  * where blocks sit in the pool. Per call (and per 1024 sequences): one kernel,

@@ -790,6 +790,9 @@ int tree_impl(bool fp8, void *out, const void *q, const void *k_cache, const voi
     if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffff ||
         static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffff)
         return fail(PKV_ERR_INVALID_ARGUMENT, "pool or table too large: blocks * block_size must be < 2^31");
+    // the kernel counts positions to the end of an iteration of 64 in 32 bits
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffff - 63)
+        return fail(PKV_ERR_INVALID_ARGUMENT, "table too large: max_blocks_per_seq * block_size must be <= 2^31 - 64");
     if (max_query_len > PKV_MAX_TREE_TOKENS)
         return fail(PKV_ERR_UNSUPPORTED, "max_query_len %d exceeds %d", max_query_len, PKV_MAX_TREE_TOKENS);
     if (max_query_len > static_cast<int64_t>(mask_words) * 32)
