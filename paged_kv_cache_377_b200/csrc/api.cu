@@ -966,6 +966,8 @@ int kv_tables_trim(const int32_t *block_tables, const int32_t *context_lens, con
     if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffff ||
         static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffff)
         return fail(PKV_ERR_INVALID_ARGUMENT, "pool or table too large: blocks * block_size must be < 2^31");
+    if (num_blocks == 0x7fffffff)  // the kernel's sums saturate there: it could not tell all blocks from more
+        return fail(PKV_ERR_INVALID_ARGUMENT, "pool too large: num_blocks must be < 2^31 - 1");
     const cudaError_t e =
         pkv::tables_trim_launch(block_tables, context_lens, keep_lens, free_blocks, num_free, num_free_out, num_seqs,
                                 max_blocks_per_seq, block_size, num_blocks, d_status, static_cast<cudaStream_t>(stream));

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kTableThreads)
                     const int i = find_start(sm.tok, count, t);
                     const int have = blocks_of(sm.len[i], block_size);
                     int32_t *row = block_tables + static_cast<int64_t>(s0 + i) * max_blocks_per_seq;
-                    const int pos = sm.len[i] + t - sm.tok[i];
+                    const int pos = sm.len[i] + (t - sm.tok[i]);
                     const int lb = pos / block_size, off = pos - lb * block_size;
                     const int p = lb < have ? row[lb] : free_blocks[top - 1 - (blk0 + sm.blk[i] + lb - have)];
                     if (lb >= have && off == 0) row[lb] = p;
@@ -297,19 +297,21 @@ __global__ void __launch_bounds__(kTableThreads)
         sm.tok[tid] = static_cast<int>(gone);
         sm.len[tid] = first;
         __syncthreads();
-        const int run = static_cast<int>(tg) > 2 * ctas * kTableThreads ? kRun : 1;
-        for (int k0 = (rank * kTableThreads + tid) * run; k0 < static_cast<int>(tg); k0 += ctas * kTableThreads * run) {
+        const uint32_t run = tg > 2u * ctas * kTableThreads ? kRun : 1;
+        // (unsigned: a step past 2^31 - 1 blocks has to end the loop)
+        for (uint32_t b0 = (rank * kTableThreads + tid) * run; b0 < tg; b0 += ctas * kTableThreads * run) {
+            const int k0 = static_cast<int>(b0), left = static_cast<int>(min(tg - b0, run));
             int i = find_start(sm.tok, count, k0), p[kRun];
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
                 const int k = k0 + j;
-                if (j >= run || k >= static_cast<int>(tg)) break;
+                if (j >= left) break;
                 while (i + 1 < count && sm.tok[i + 1] <= k) ++i;
                 p[j] = block_tables[static_cast<int64_t>(s0 + i) * max_blocks_per_seq + sm.len[i] + k - sm.tok[i]];
             }
 #pragma unroll
             for (int j = 0; j < kRun; ++j) {
-                if (j >= run || k0 + j >= static_cast<int>(tg)) break;
+                if (j >= left) break;
                 if (p[j] < 0 || p[j] >= num_blocks) {
                     atomicOr(status, PKV_STATUS_BAD_BLOCK_ID);
                     p[j] = -1;

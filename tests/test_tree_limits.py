@@ -1,7 +1,8 @@
 """The largest sizes that the drafted-tree calls take: one step further is refused before any CUDA call."""
 import pytest
 
-from test_tree_abi import _tree, err
+from paged_kv_cache_377_b200 import tree
+from test_tree_abi import P, _tree, err
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -14,3 +15,17 @@ def test_tables_whose_last_iteration_passes_32_bits(bs, fp8):
     for mb in sorted({most + 1, last}):
         assert mb * bs <= 2 ** 31 - 1
         assert _tree(fp8, MB=mb, bs=bs) == -1 and "2^31 - 64" in err(), err()
+
+
+def test_a_pool_of_as_many_blocks_as_sums_saturate_at():
+    args = [P] * 6 + [4, 8, 1, 2 ** 31 - 1, P, None]
+    assert tree._lib().kv_tables_trim(*args) == -1 and "2^31 - 1" in err(), err()
+
+
+def test_steps_over_the_blocks_of_the_largest_pool_end():
+    """The trim kernel's loop in its own 32-bit arithmetic: 8 CTAs of 1024 threads, four blocks a thread. Signed, the
+    step behind the last block of the largest pool is negative, and the loop goes on."""
+    blocks, step = 2 ** 31 - 2, 8 * 1024 * 4
+    last = (blocks - 1) // step * step               # thread 0's last turn
+    assert not (last + step) % 2 ** 32 < blocks
+    assert (last + step + 2 ** 31) % 2 ** 32 - 2 ** 31 < blocks
