@@ -100,17 +100,30 @@ def library_path() -> str:
     return _build.LIB
 
 
-def _ensure_built() -> str:
-    """Builds the library with nvcc when it is missing or older than its sources."""
-    if not _build.is_stale():
-        return _build.LIB
+def _ensure(stale, build) -> None:
+    """Builds what is missing or out of date, once where several processes find it so."""
+    if not stale():
+        return
     os.makedirs(_build.BUILD, exist_ok=True)
     with open(os.path.join(_build.BUILD, ".lock"), "w") as lk:
         fcntl.flock(lk, fcntl.LOCK_EX)
         try:
-            return _build.build()
+            if stale():
+                build()
         finally:
             fcntl.flock(lk, fcntl.LOCK_UN)
+
+
+def _ensure_built() -> str:
+    """Builds the library with nvcc when it is missing or older than its sources."""
+    _ensure(_build.is_stale, _build.build)
+    return _build.LIB
+
+
+def _ensure_marshal() -> None:
+    """Builds _marshal.so (its callers load the library first) when it is missing, older than its sources or for another
+    torch or Python."""
+    _ensure(_build.marshal_is_stale, _build.build_marshal)
 
 
 def library() -> ctypes.CDLL:

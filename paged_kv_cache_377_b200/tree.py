@@ -43,10 +43,12 @@ def _lib() -> ctypes.CDLL:
 
 
 def _calls():
-    """The module that checks the arguments and makes the calls (csrc/marshal.cpp)."""
+    """The module that checks the arguments and makes the calls (csrc/marshal.cpp), built first if needed. Raises
+    where it cannot be; no call of the other modules needs it."""
     global _marshal
     if _marshal is None:
         _lib()
+        b._ensure_marshal()
         from . import _marshal as module
         _marshal = module
     return _marshal
