@@ -86,3 +86,30 @@ def test_bad_blocks_in_cut_contexts(name, bad, fp8):
     out, st = run(step)
     assert st == pkv.PKV_STATUS_BAD_BLOCK_ID
     assert excess(out, ref, square, fp8) < 1
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("hq,nodes_hi", [(1, 3), (8, 40)])
+def test_more_sequences_than_one_launch_takes_with_cut_contexts(hq, nodes_hi, fp8):
+    """Two launches (over e4m3 pools three), each with contexts that are cut and joined, one behind the other."""
+    rng = np.random.default_rng(131)
+    base, nodes = rng.integers(0, 20, size=1100), rng.integers(0, 3, size=1100)
+    base[[0, 511, 512, 700, 1023, 1024, 1099]] = [2500, 1900, 2100, 1300, 900, 2222, 1777]
+    nodes[[0, 511, 512, 700, 1023, 1024, 1099]] = [nodes_hi, 1, nodes_hi, 2, nodes_hi, 3, nodes_hi]
+    step = make_step(133, base, nodes, hq, 1, 64, 16, fp8=fp8, tail_rows=2)
+    out, st = run(step)
+    assert st == 0
+    ref, square = moments(step)
+    live = int(step.query_start[-1])
+    assert excess(out[:live], ref[:live], square[:live], fp8) < 1
+    assert (out[live:] == out[-1, 0, 0]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_as_many_drafts_as_a_sequence_may_bring(fp8):
+    """4096 drafts of one sequence, beside one of the others."""
+    step = make_step(135, [5, 700], [4096, 3], 2, 1, 64, 32, fp8=fp8)
+    out, st = run(step)
+    assert st == 0
+    ref, square = moments(step)
+    assert excess(out, ref, square, fp8) < 1
