@@ -26,6 +26,7 @@ import datetime
 import hashlib
 import json
 import os
+import re
 import statistics
 import sys
 import threading
@@ -129,22 +130,27 @@ def measured_peaks():
     return FALLBACK_HBM_GBS, "fallback"
 
 
-def decode_sources_sha():
+def code_sha(paths):
+    """Hash of C++ sources without their comments and layout: what a capture was taken on stays the same when only
+    those change."""
     h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "paged_kv_cache_377_b200", "csrc")
-    for name in ("decode.cu", "decode_common.cuh", "device_utils.cuh"):
-        with open(os.path.join(csrc, name), "rb") as f:
-            h.update(f.read())
+    for path in paths:
+        with open(path) as f:
+            code = re.sub(r"//[^\n]*|/\*.*?\*/", " ", f.read(), flags=re.S)
+        h.update(" ".join(code.split()).encode())
     return h.hexdigest()[:16]
+
+
+def sources_sha(names):
+    return code_sha([os.path.join(ROOT, "paged_kv_cache_377_b200", "csrc", name) for name in names])
+
+
+def decode_sources_sha():
+    return sources_sha(("decode.cu", "decode_common.cuh", "device_utils.cuh"))
 
 
 def prefill_sources_sha():
-    h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "paged_kv_cache_377_b200", "csrc")
-    for name in ("prefill_tc.cu", "tcgen05_utils.cuh", "step_utils.cuh", "device_utils.cuh"):
-        with open(os.path.join(csrc, name), "rb") as f:
-            h.update(f.read())
-    return h.hexdigest()[:16]
+    return sources_sha(("prefill_tc.cu", "tcgen05_utils.cuh", "step_utils.cuh", "device_utils.cuh"))
 
 
 def profiled_prefill_traffic(workload: str):

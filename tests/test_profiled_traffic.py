@@ -41,3 +41,12 @@ def test_the_hash_covers_every_header_of_the_kernel():
     hashed = inspect.getsource(bench.prefill_sources_sha)
     for name in closure("prefill_tc.cu", set()):
         assert f'"{name}"' in hashed, name
+
+
+def test_comments_and_layout_are_not_code(tmp_path):
+    a, b, c = (tmp_path / x for x in "abc")
+    a.write_text("int f() { return 1; }  // one\n")
+    b.write_text("/* what\n it does */\nint f() {\n    return 1;\n}\n")
+    c.write_text("int f() { return 2; }  // one\n")
+    assert bench.code_sha([a]) == bench.code_sha([b]) != bench.code_sha([c])
+    assert bench.code_sha([a, c]) != bench.code_sha([c, a])
