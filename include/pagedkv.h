@@ -458,7 +458,9 @@ int kv_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
  *               several graphs in turn); calls that may overlap need one each.
  * A sequence whose query_start or context length is inconsistent is skipped
  * (its rows are left as they were) and sets PKV_STATUS_BAD_CONTEXT_LEN; a bad
- * table entry sets PKV_STATUS_BAD_BLOCK_ID and its positions are not seen.
+ * table entry sets PKV_STATUS_BAD_BLOCK_ID and its positions are not seen. With
+ * num_seqs, num_tokens or max_query_len 0 there is no draft: the call returns at
+ * once and looks at nothing on the device.
  * Supported: as paged_attn_decode (head_dim 64 / 128, block_size 16 / 32, group
  * <= 8), with any number of sequences and block tables of up to 2^31 - 64 tokens. bf16
  * products and fp32 sums on tcgen05, probabilities rounded to bf16. For a given
@@ -470,7 +472,8 @@ int kv_cache_append(const void *k, const void *v, void *k_cache, void *v_cache,
  * paged_attn_tree_fp8: the same over e4m3 pools with per-kv-head scales (and per
  * 512 sequences). Q is scaled per row by a power of two and split into two e4m3
  * terms (eight bits); K's codes are multiplied as they are, V's widened to f16,
- * exactly, and probabilities rounded to f16.
+ * exactly, and probabilities rounded to f16, a row's largest kept between 2^7 and
+ * 2^15: weights below 2^-32 of it are lost, those below 2^-21 lose bits.
  */
 #define PKV_MAX_TREE_TOKENS 4096
 int pkv_tree_workspace_bytes(int head_dim, size_t *bytes);
@@ -498,7 +501,8 @@ int paged_attn_tree_fp8(void *out, const void *q, const void *k_cache, const voi
  * sequence are left as they were. A parent that is neither -1 nor an earlier
  * draft counts as -1 and sets PKV_STATUS_BAD_TREE in *d_status; a sequence
  * whose query_start is inconsistent (or longer than max_query_len <=
- * mask_words * 32) is skipped and sets PKV_STATUS_BAD_CONTEXT_LEN.
+ * mask_words * 32) is skipped and sets PKV_STATUS_BAD_CONTEXT_LEN. With num_seqs,
+ * num_tokens or max_query_len 0 the call returns at once, as paged_attn_tree does.
  */
 int paged_tree_mask(int32_t *tree_mask, int32_t *depths, const int32_t *parents, const int32_t *query_start,
                     int num_seqs, int num_tokens, int max_query_len, int mask_words, int32_t *d_status,
@@ -545,6 +549,7 @@ int kv_tables_grow(int32_t *block_tables, const int32_t *context_lens, const int
  * stack that would overflow (a block given back twice) PKV_STATUS_BAD_BLOCK_ID,
  * and nothing changes. An entry outside the pool goes onto the stack as -1 and
  * sets PKV_STATUS_BAD_BLOCK_ID. Blocks shared with another table must be kept.
+ * num_blocks is less than 2^31 - 1.
  */
 int kv_tables_trim(const int32_t *block_tables, const int32_t *context_lens, const int32_t *keep_lens,
                    int32_t *free_blocks, const int32_t *num_free, int32_t *num_free_out, int num_seqs,

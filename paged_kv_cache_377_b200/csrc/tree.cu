@@ -144,8 +144,9 @@ struct TreeShape {
 // A warp's `span` rows of codes (dense, D bytes each) into rows tok0 .. of an operand tile ([64-column half][row][128
 // bytes], swizzled), as f16 (exact). Eight rows of four 16-code chunks a step; rows and halves alternate so that neither
 // side's banks meet; four steps' codes are loaded before the first is stored, so that their latencies overlap.
-// The hardware's conversion takes two codes in 2.0 cycles a warp; placing their bits by hand takes several integer
-// instructions of 2.2 to 2.8 each.
+// The hardware's conversion of two codes takes 2.0 cycles of a scheduler per warp instruction (63 lanes per SM-clock; 16
+// independent values a thread, one to eight warps a scheduler), as one byte permute or one logic operation does:
+// placing the bits by hand takes several of those.
 template <int D>
 __device__ __forceinline__ void widen_rows(const uint8_t *src, uint8_t *dst, int tok0, int span, int lane) {
     constexpr int HALVES = D / 64, BATCH = 4;
