@@ -565,7 +565,8 @@ int kv_tables_trim(const int32_t *block_tables, const int32_t *context_lens, con
  *               rising order, each in [0, n_s)
  * num_accepted  device int32 [num_seqs]: 0 .. min(n_s, max_accepted)
  * new_lens      device int32 [num_seqs] or NULL: base + num_accepted[s]; not
- *               context_lens, which the other layers' calls still read
+ *               context_lens, which the other layers' calls still read, nor any
+ *               other input's memory
  * A sequence with a path that does not rise or leaves its drafts
  * (PKV_STATUS_BAD_TREE), bad lengths (PKV_STATUS_BAD_CONTEXT_LEN) or a bad
  * table entry (PKV_STATUS_BAD_BLOCK_ID) keeps its rows, and new_lens[s] =

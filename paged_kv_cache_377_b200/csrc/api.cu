@@ -727,6 +727,12 @@ int kv_block_copy(void *k_cache, void *v_cache, const int32_t *src, const int32_
 
 namespace {
 
+// Whether a's n words and b's m words share any (NULL shares none).
+bool overlap(const int32_t *a, int64_t n, const int32_t *b, int64_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + m * sizeof(int32_t) && y < x + n * sizeof(int32_t);
+}
+
 // Tree workspace: [0, 256) header (status word at 0) | the CTAs' cut segments | counters of two-piece segments | rows' maxima and sums of the
 // partials | their fp32 rows: two partials of 128 rows for each of kTreeMaxCtas CTAs.
 struct TreeLayout {
@@ -1000,6 +1006,12 @@ int kv_cache_keep(void *k_cache, void *v_cache, const int32_t *block_tables, con
         return fail(PKV_ERR_INVALID_ARGUMENT, "k_cache and v_cache must be 16-byte aligned");
     if (new_lens == context_lens)
         return fail(PKV_ERR_INVALID_ARGUMENT, "new_lens must not be context_lens: the next layer still reads them");
+    // one CTA of a sequence writes its length while others may not have read what it follows from
+    const int64_t S = num_seqs;
+    if (overlap(new_lens, S, context_lens, S) || overlap(new_lens, S, num_accepted, S) ||
+        overlap(new_lens, S, query_start, S + 1) || overlap(new_lens, S, accepted, S * max_accepted) ||
+        overlap(new_lens, S, block_tables, S * max_blocks_per_seq))
+        return fail(PKV_ERR_INVALID_ARGUMENT, "new_lens must not overlap an input");
     const cudaError_t e = pkv::cache_keep_launch(
         k_cache, v_cache, block_tables, context_lens, query_start, accepted, num_accepted, new_lens, num_seqs,
         max_accepted, static_cast<int>(row_bytes), block_size, max_blocks_per_seq, num_blocks, d_status,

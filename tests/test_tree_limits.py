@@ -1,4 +1,6 @@
 """The largest sizes that the drafted-tree calls take: one step further is refused before any CUDA call."""
+import ctypes
+
 import pytest
 
 from paged_kv_cache_377_b200 import tree
@@ -29,3 +31,14 @@ def test_steps_over_the_blocks_of_the_largest_pool_end():
     last = (blocks - 1) // step * step               # thread 0's last turn
     assert not (last + step) % 2 ** 32 < blocks
     assert (last + step + 2 ** 31) % 2 ** 32 - 2 ** 31 < blocks
+
+
+@pytest.mark.parametrize("at,words", [(3, 4), (4, 5), (5, 32), (6, 4), (2, 32)])
+@pytest.mark.parametrize("end", ["first", "last"])
+def test_new_lengths_in_an_inputs_memory_are_refused(at, words, end):
+    """context_lens, query_start, accepted, num_accepted, block_tables: a CTA writes a length that others of its
+    sequence have not read the inputs of yet. One word in common is enough."""
+    args = [P, P, *(ctypes.c_void_p(1 << (20 + i)) for i in range(6)), 4, 8, 2, 64, 2, 16, 8, 64, P, None]
+    start = args[at].value
+    args[7] = ctypes.c_void_p(start - 12 if end == "first" else start + 4 * (words - 1))
+    assert tree._lib().kv_cache_keep(*args) == -1 and "new_lens" in err(), err()
