@@ -762,9 +762,12 @@ __global__ void __launch_bounds__(TreeShape<D, FP8>::kThreads, 2)
                         for (int e = 0; e < 4; ++e) m4[e] = fmaxf(m4[e], x[60 + e]);
                         mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
                     }
-                    // the reference, kLift below a maximum, moves only when that would be exceeded by more than 2^8
+                    // The reference, kLift below a maximum, moves only when that would be exceeded by more than 2^8. (f16: at
+                    // any excess from 2^20 on, where what the products here are rounded by would use up what is left of
+                    // its range; so it lasts to 2^26.)
                     float m_new = m_ref;
-                    if (mx * c2 > m_ref + (kLift + 8.f)) m_new = mx * c2 - kLift;
+                    const float top = mx * c2, lag = FP8 && fabsf(top) >= 0x1p20f ? 0.f : 8.f;
+                    if (top > m_ref + (kLift + lag)) m_new = top - kLift;
                     const float shift = m_new == -INFINITY ? 0.f : -m_new;  // a row that has seen nothing: P = 0
                     const float2 cc = make_float2(c2, c2), nm = make_float2(shift, shift);
                     float2 ps2a = make_float2(0.f, 0.f), ps2b = make_float2(0.f, 0.f);

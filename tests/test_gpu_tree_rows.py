@@ -6,6 +6,7 @@ import torch
 
 from test_gpu_tree import check, run
 from tree_reference import assert_close, attention, make_step
+from tree_strict import excess, moments
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +70,27 @@ def test_a_query_that_is_not_finite_stays_in_its_row(value, fp8):
     assert (out[[blind[0], blind[2]]] == 0).all()
     assert np.isnan(out[[seeing[0], seeing[2], 43]]).all()
     assert_close(out[~hit], ref[~hit], spread[~hit], fp8, "the rows beside")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("power", [10, 18, 20, 22, 23, 24, 25])
+def test_logits_far_from_zero(power, fp8):
+    """Logits around 2^power (in powers of two) that grow by 2^(power - 23) from one run of 64 tokens to the next, where a
+    step of fp32 grows to 4: the largest weight must not leave f16's range, however the running maximum was rounded. The
+    products are exact, S = 2^21 + d / 4 with d in 0 .. 15, so that the weights are as well known as elsewhere."""
+    step = make_step(99, [1200, 90, 3000], [9, 16, 5], 4, 2, 64, 16, fp8=fp8, scale=2.0 ** (power - 21) * np.log(2))
+    step.q[:] = 0
+    step.q[..., :8] = 2.0 ** 10
+    step.q[..., 8] = 0.25
+    step.k_scale[:] = 1
+    for s in range(3):
+        t = torch.arange(int(step.context_lens[s]))
+        rows = torch.zeros(len(t), 2, 64)
+        rows[..., :8] = 256
+        rows[..., 8] = (t // 64 % 16)[:, None].float()
+        keys = rows.to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else rows.to(torch.bfloat16)
+        step.k_cache[step.block_tables[s].long()[t // 16], t % 16] = keys
+    out, st = run(step)
+    assert st == 0
+    ref, square = moments(step)
+    assert excess(out, ref, square, fp8) < 1
