@@ -1,4 +1,4 @@
-"""Starts of a step's rows that no difference of two words can judge: every call that takes them skips the sequence,
+"""Starts of a step's rows that a 32-bit difference mistakes for lengths: every call that takes them skips the sequence,
 flags it and leaves the others as they are."""
 import numpy as np
 import pytest
